@@ -138,6 +138,8 @@ typedef struct {
                          output row and partial slot of that kernel past its buffer, so that
                          the checks skip each store and set MLA_DEV_BOUNDS; refused on other
                          plans */
+  int32_t sinks;     /* first keys that stay visible with a window (0 = none); set with
+                        mla_decode_plan_sinks */
 } mla_plan;
 
 /*
@@ -172,6 +174,23 @@ int mla_decode_plan_custom(int batch, int q_len, int num_heads, int max_seq_len,
  * window < 0), MLA_ERR_PLAN_MISMATCH (plan not from mla_decode_plan*).
  */
 int mla_decode_plan_window(mla_plan* plan, int window);
+
+/*
+ * mla_decode_plan_sinks: with a sliding window, keep the first `sinks` keys of
+ * every sequence visible too (attention sinks; no counterpart on the pages: an
+ * addition of this library). A row with n visible keys then attends to keys
+ * [0, min(sinks, n)) and [max(0, n - window), n), each key once. Without a
+ * window (window = 0) every key is visible and sinks change nothing; the two
+ * setters may come in either order. sinks = 0 restores the plain window.
+ *
+ * Pages that hold no key any query row of the call sees are not read, and
+ * their block-table entries are not looked at, so a caller may give the pages
+ * between the sinks and the window back. FP8 plans send P as two E4M3 terms
+ * whatever the window's length. Supported by the kernels that take a window
+ * (MLA_ERR_UNSUPPORTED_SHAPE otherwise); the workspace size does not change.
+ * Errors: MLA_ERR_INVALID_ARG (null plan, sinks < 0), MLA_ERR_PLAN_MISMATCH.
+ */
+int mla_decode_plan_sinks(mla_plan* plan, int sinks);
 
 /*
  * mla_decode: one decode step (tokenspeed-mla package card, "Quickstart":
@@ -403,6 +422,98 @@ int mla_kv_pack(const void* latent, const void* rope, int64_t n_tokens, const in
  */
 int mla_kv_amax(const void* latent, const void* rope, int64_t n_tokens, int in_dtype, float* amax,
                 void* stream);
+
+/*
+ * mla_key_weights: the attention weight each cached key received in one decode
+ * or prefill step, accumulated over the step's query rows (an addition of this
+ * library; what an eviction by accumulated attention weight goes by):
+ *
+ *   weights_out[b, j] = decay * weights_in[b, j]
+ *                       + sum over rows (t, h) of entry b that see key j of
+ *                         exp(softmax_scale * q . k_j - lse[row])
+ *
+ * for every key j < seq_lens[b]; columns from seq_lens[b] on are left as they
+ * were. Call it after mla_decode (or mla_prefill) with that call's plan, q,
+ * cache, tables and lse: causal mask, window and sinks are the plan's. A row
+ * whose lse is -inf (no visible key) adds nothing.
+ *
+ *   plan          a decode plan, or with cu_seqlens_q a prefill plan. Kernel
+ *                 MLA_KERNEL_SIMT takes the plain CUDA-core form; every other
+ *                 kernel the tensor-core form
+ *   q, total_q, cu_seqlens_q
+ *                 as mla_prefill; a decode plan takes cu_seqlens_q = NULL and
+ *                 ignores total_q
+ *   kv_cache .. kv_scale   as mla_decode
+ *   lse           device fp32 [B, q_len, H] or [total_q, H], as written by the
+ *                 attention call
+ *   weights_in    device fp32, row b at weights_in + b * in_stride; NULL stands
+ *                 for zeros. Not read when decay is 0. May be weights_out
+ *   decay         finite, >= 0
+ *   weights_out   device fp32, row b at weights_out + b * out_stride
+ *   cols          columns of both, >= min(plan->max_seq_len,
+ *                 max_pages_per_seq * 64); the strides are >= cols
+ *   device_status device int32 word (a decode workspace's status word, say),
+ *                 into which MLA_DEV_* bits are OR-ed; it is not cleared
+ *
+ * Sums are fp32 in a fixed order: the same inputs give the same bits. A key on
+ * a page outside [0, num_pages) receives nothing and sets MLA_DEV_BAD_PAGE.
+ * No workspace; nothing is allocated or synchronised; capturable in a CUDA
+ * graph. Errors as mla_decode, before any launch.
+ */
+int mla_key_weights(const mla_plan* plan, const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                    const void* kv_cache, int64_t num_pages, int page_size, const int32_t* block_tables,
+                    int max_pages_per_seq, const int32_t* seq_lens, float softmax_scale, float q_scale,
+                    float kv_scale, const float* lse, const float* weights_in, int64_t in_stride, float decay,
+                    float* weights_out, int64_t out_stride, int64_t cols, int32_t* device_status, void* stream);
+
+/*
+ * mla_cache_evict: cut every sequence to at most `budget` keys and gather the
+ * rows that stay onto pages of another block table (an addition of this
+ * library). Of entry b's n = seq_lens[b] keys stay: all if n <= budget;
+ * otherwise the first `sinks`, the last `recent`, and of those between the
+ * budget - sinks - recent with the largest weights. Equal weights: the lower
+ * position stays; NaN counts as the lowest weight. The keys that stay keep
+ * their order, and row i of the result lies at out page i / 64, offset i % 64.
+ *
+ *   weights, weights_stride, cols
+ *                 device fp32, row b at weights + b * weights_stride, with
+ *                 cols columns (<= weights_stride)
+ *   seq_lens      device int32 [batch]; a length below 0 or above cols or the
+ *                 table is clamped and sets MLA_DEV_SEQ_TOO_LONG
+ *   kv_cache, num_pages, page_size, block_tables, max_pages_per_seq
+ *                 the cache, as mla_decode; only rows that stay are read
+ *   out_cache, out_num_pages, out_block_tables, out_max_pages_per_seq
+ *                 where they go: a cache of the same type (it may be the same
+ *                 one) and its table, out_max_pages_per_seq * 64 >= budget.
+ *                 The pages named for an entry's result must be distinct from
+ *                 each other, from other entries' and from every page of
+ *                 block_tables (the same table for both is refused): shared
+ *                 prefix pages then stay as they are for their other readers.
+ *                 The rest of an entry's last page is set to zero, so that the
+ *                 attention, which reads whole pages, meets finite values
+ *   dtype         of both caches (rows move as they are: FP8 keeps its scale)
+ *   out_seq_lens  device int32 [batch]: min(n, budget); may be seq_lens
+ *   kept          device int32 [batch, budget]: the positions that stay,
+ *                 ascending, then -1
+ *   out_weights   device fp32, row b at out_weights + b * out_weights_stride
+ *                 (>= budget): the weights of the keys that stay; columns from
+ *                 the new length on are left as they were. NULL: not written.
+ *                 It must not overlap weights
+ *   device_status optional int32 device word, as mla_kv_pack. A page index out
+ *                 of range sets MLA_DEV_BAD_PAGE: such a source row arrives as
+ *                 zeros, such a destination row is skipped
+ *
+ * Nothing is allocated or synchronised; capturable in a CUDA graph. Errors:
+ * MLA_ERR_INVALID_ARG (budget < 1, sinks + recent > budget, overlaps, null or
+ * misaligned pointers), MLA_ERR_UNSUPPORTED_SHAPE, MLA_ERR_ARCH, MLA_ERR_CUDA.
+ * batch = 0 is a no-op.
+ */
+int mla_cache_evict(const float* weights, int64_t weights_stride, int64_t cols, const int32_t* seq_lens, int batch,
+                    int budget, int sinks, int recent, const void* kv_cache, int64_t num_pages, int page_size,
+                    const int32_t* block_tables, int max_pages_per_seq, void* out_cache, int64_t out_num_pages,
+                    const int32_t* out_block_tables, int out_max_pages_per_seq, int dtype, int32_t* out_seq_lens,
+                    int32_t* kept, float* out_weights, int64_t out_weights_stride, int32_t* device_status,
+                    void* stream);
 
 #ifdef __cplusplus
 }

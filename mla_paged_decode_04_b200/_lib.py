@@ -34,7 +34,8 @@ EXPORTED = ["mla_decode_plan", "mla_decode_plan_custom", "mla_decode", "mla_deco
             "mla_decode_combine", "mla_decode_status", "mla_status_string", "mla_version",
             "mla_decode_no_alloc", "mla_decode_no_alloc_status", "mla_last_cuda_error", "mla_kv_pack", "mla_kv_amax",
             "mla_decode_plan_window", "mla_prefill_plan", "mla_prefill_plan_custom", "mla_prefill",
-            "mla_prefill_partial", "mla_prefill_combine", "mla_bounds_checked"]
+            "mla_prefill_partial", "mla_prefill_combine", "mla_bounds_checked",
+            "mla_decode_plan_sinks", "mla_key_weights", "mla_cache_evict"]
 MLA_NO_ALLOC_SCRATCH_BYTES = 48 << 20
 
 
@@ -48,6 +49,7 @@ class MlaPlan(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64), ("partial_offset", ctypes.c_uint64),
         ("lse_offset", ctypes.c_uint64), ("magic", ctypes.c_uint32), ("schedule", ctypes.c_uint32),
         ("window", ctypes.c_int32), ("varlen", ctypes.c_int32), ("fault_test", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
     ]
 
     def as_dict(self):
@@ -105,6 +107,14 @@ def load_library(path):
     lib.mla_kv_pack.restype = i32
     lib.mla_kv_amax.argtypes = [vp, vp, i64, i32, vp, vp]
     lib.mla_kv_amax.restype = i32
+    lib.mla_decode_plan_sinks.argtypes = [P, i32]
+    lib.mla_decode_plan_sinks.restype = i32
+    lib.mla_key_weights.argtypes = [P, vp, i64, vp, vp, i64, i32, vp, i32, vp, f32, f32, f32, vp, vp, i64, f32, vp,
+                                    i64, i64, vp, vp]
+    lib.mla_key_weights.restype = i32
+    lib.mla_cache_evict.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, vp, i64, i32, vp, i32, vp, i64, vp, i32,
+                                    i32, vp, vp, vp, i64, vp, vp]
+    lib.mla_cache_evict.restype = i32
     lib.mla_bounds_checked.argtypes = []
     lib.mla_bounds_checked.restype = i32
     return lib
@@ -173,6 +183,14 @@ def mla_decode_plan_window(plan: MlaPlan, window: int) -> MlaPlan:
     rc = _lib.mla_decode_plan_window(ctypes.byref(plan), int(window))
     if rc != 0:
         raise MlaError(rc, "mla_decode_plan_window")
+    return plan
+
+
+def mla_decode_plan_sinks(plan: MlaPlan, sinks: int) -> MlaPlan:
+    """Keep the first `sinks` keys visible beside the plan's window, in place (0 = none), and return it."""
+    rc = _lib.mla_decode_plan_sinks(ctypes.byref(plan), int(sinks))
+    if rc != 0:
+        raise MlaError(rc, "mla_decode_plan_sinks")
     return plan
 
 
@@ -336,6 +354,111 @@ def kv_amax(latent, rope, out=None, stream=None) -> torch.Tensor:
     return out
 
 
+def _weight_rows(name, t, device):
+    """Checks an fp32 [B, columns] tensor whose rows may lie apart; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != torch.float32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be float32 [batch, columns] with adjacent columns")
+    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+
+
+def key_weights(plan: MlaPlan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, device_status,
+                weights=None, decay=1.0, q_scale=1.0, kv_scale=1.0, cu_seqlens_q=None, stream=None) -> torch.Tensor:
+    """The attention weight every cached key received in one step: out[b, j] = decay * weights[b, j] + the sum of
+    exp(scaled score - lse) over the step's rows that see key j, for j < seq_lens[b] (the rest of `out` stays).
+
+    Pass the plan, q, cache, tables and lse of the attention call it follows (cu_seqlens_q too for a prefill plan).
+    `weights` and `out` are fp32 [B, columns] (rows may be strided) and may be the same tensor; weights = None counts
+    as zeros. device_status: an int32 device word for MLA_DEV_* bits. See include/mla_decode.h.
+    """
+    _check_tensors(q, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, lse=lse,
+                   cu_seqlens_q=cu_seqlens_q, device_status=device_status)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if q.dtype != kv_cache.dtype or _dtype_code(q.dtype) != plan.dtype:
+        raise ValueError("q and kv_cache must have the plan's dtype")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != 576 or q.shape[-1] != 576:
+        raise ValueError("q and kv_cache must have 576 dims")
+    rows = q.numel() // 576
+    if not plan.varlen and rows != plan.batch * plan.q_len * plan.num_heads:
+        raise ValueError("q must be [batch, q_len, num_heads, 576] of the plan")
+    if plan.varlen and (q.dim() != 3 or q.shape[1] != plan.num_heads):
+        raise ValueError("q must be [total_q, num_heads, 576]")
+    if cu_seqlens_q is not None and (cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.numel() != plan.batch + 1):
+        raise ValueError("cu_seqlens_q must be int32 [batch + 1]")
+    if lse is None or lse.dtype != torch.float32 or lse.numel() != rows:
+        raise ValueError("lse must be float32 with one value per query row")
+    if device_status is None or device_status.dtype != torch.int32:
+        raise ValueError("device_status must be an int32 CUDA tensor")
+    if block_tables.dim() != 2 or block_tables.shape[0] != plan.batch or seq_lens.numel() != plan.batch:
+        raise ValueError("block_tables and seq_lens must have one row per batch entry")
+    out_stride = _weight_rows("out", out, q.device)
+    in_stride, cols = 0, int(out.shape[1])
+    if weights is not None:
+        in_stride = _weight_rows("weights", weights, q.device)
+        if weights.shape != out.shape:
+            raise ValueError("weights and out must have one shape")
+    if out.shape[0] != plan.batch:
+        raise ValueError("out must have one row per batch entry")
+    rc = _lib.mla_key_weights(ctypes.byref(plan), _ptr(q), int(q.shape[0]), _ptr(cu_seqlens_q), _ptr(kv_cache),
+                              int(kv_cache.shape[0]), int(kv_cache.shape[1]), _ptr(block_tables),
+                              int(block_tables.shape[1]), _ptr(seq_lens), float(softmax_scale), float(q_scale),
+                              float(kv_scale), _ptr(lse), _ptr(weights), in_stride, float(decay), _ptr(out),
+                              out_stride, cols, _ptr(device_status), ctypes.c_void_p(_stream_of(q, stream)))
+    if rc != 0:
+        raise MlaError(rc, "mla_key_weights")
+    return out
+
+
+def cache_evict(weights, seq_lens, kv_cache, block_tables, out_cache, out_block_tables, budget, sinks=0, recent=0,
+                out_seq_lens=None, kept=None, out_weights=None, device_status=None, stream=None):
+    """Cut every sequence to at most `budget` keys: the first `sinks`, the last `recent` and, between them, those
+    with the largest `weights` (fp32 [B, columns]); the rows that stay move, in order, to the pages of
+    out_block_tables in out_cache (which may be kv_cache, on pages block_tables does not name).
+
+    Returns (out_seq_lens int32 [B], kept int32 [B, budget]: the positions that stay, then -1, out_weights fp32
+    [B, budget]: their weights); each is allocated when not given. See include/mla_decode.h.
+    """
+    _check_tensors(seq_lens, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, out_cache=out_cache,
+                   out_block_tables=out_block_tables, out_seq_lens=out_seq_lens, kept=kept,
+                   device_status=device_status)
+    B, budget = int(seq_lens.numel()), int(budget)
+    if kv_cache.dtype != out_cache.dtype or kv_cache.dim() != 3 or out_cache.dim() != 3 or \
+            kv_cache.shape[2] != 576 or out_cache.shape[1:] != kv_cache.shape[1:]:
+        raise ValueError("kv_cache and out_cache must be [pages, 64, 576] of one dtype")
+    if out_block_tables.dtype != torch.int32:
+        raise ValueError("out_block_tables must be int32")
+    if block_tables.dim() != 2 or out_block_tables.dim() != 2 or block_tables.shape[0] != B or \
+            out_block_tables.shape[0] != B or weights.shape[0] != B:
+        raise ValueError("weights and the block tables must have one row per batch entry")
+    stride = _weight_rows("weights", weights, seq_lens.device)
+    if budget < 1:
+        raise MlaError(MLA_ERR_INVALID_ARG, "mla_cache_evict")
+    if out_seq_lens is None:
+        out_seq_lens = torch.empty(B, dtype=torch.int32, device=seq_lens.device)
+    if kept is None:
+        kept = torch.empty((B, budget), dtype=torch.int32, device=seq_lens.device)
+    if out_weights is None:
+        out_weights = torch.zeros((B, budget), dtype=torch.float32, device=seq_lens.device)
+    if out_seq_lens.dtype != torch.int32 or out_seq_lens.numel() != B:
+        raise ValueError("out_seq_lens must be int32 [batch]")
+    if kept.dtype != torch.int32 or kept.shape != (B, budget):
+        raise ValueError("kept must be int32 [batch, budget]")
+    out_stride = _weight_rows("out_weights", out_weights, seq_lens.device)
+    if out_weights.shape[0] != B or out_weights.shape[1] < budget:
+        raise ValueError("out_weights must be float32 [batch, >= budget]")
+    rc = _lib.mla_cache_evict(_ptr(weights), stride, int(weights.shape[1]), _ptr(seq_lens), B, budget, int(sinks),
+                              int(recent), _ptr(kv_cache), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
+                              _ptr(block_tables), int(block_tables.shape[1]), _ptr(out_cache),
+                              int(out_cache.shape[0]), _ptr(out_block_tables), int(out_block_tables.shape[1]),
+                              _dtype_code(kv_cache.dtype), _ptr(out_seq_lens), _ptr(kept), _ptr(out_weights),
+                              out_stride, _ptr(device_status), ctypes.c_void_p(_stream_of(seq_lens, stream)))
+    if rc != 0:
+        raise MlaError(rc, "mla_cache_evict")
+    return out_seq_lens, kept, out_weights
+
+
 def alloc_workspace(plan: MlaPlan, device) -> torch.Tensor:
     """A zeroed workspace tensor of plan.workspace_bytes (torch allocations are 256-byte aligned)."""
     return torch.zeros(int(plan.workspace_bytes), dtype=torch.uint8, device=device)
@@ -345,13 +468,16 @@ class MlaDecoder:
     """Plan + workspace for one decode shape; call it once per decode step."""
 
     def __init__(self, batch, q_len, num_heads, max_seq_len, dtype, device, split_kv=0, fold=0,
-                 kernel="auto", window=0):
+                 kernel="auto", window=0, sinks=0):
         self.plan = mla_decode_plan_custom(batch, q_len, num_heads, max_seq_len, dtype,
                                            split_kv, fold, kernel)
         if window:
             mla_decode_plan_window(self.plan, window)
+        if sinks:
+            mla_decode_plan_sinks(self.plan, sinks)
         self.device = torch.device(device)
         self.workspace = alloc_workspace(self.plan, self.device)
+        self._status = self.workspace[:4].view(torch.int32)  # the status word
         self.batch, self.q_len, self.num_heads = batch, q_len, num_heads
 
     def __call__(self, q, kv_cache, block_tables, seq_lens, softmax_scale, q_scale=1.0,
@@ -365,6 +491,13 @@ class MlaDecoder:
                    self.workspace, q_scale, kv_scale, stream)
         return out, lse
 
+    def key_weights(self, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, weights=None,
+                    decay=1.0, q_scale=1.0, kv_scale=1.0, stream=None):
+        """The weight every cached key received in the step that returned `lse` (see key_weights); device-side
+        problems show in status()."""
+        return key_weights(self.plan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, self._status,
+                           weights, decay, q_scale, kv_scale, stream=stream)
+
     def status(self, clear=True) -> int:
         return mla_decode_status(self.workspace, clear)
 
@@ -373,12 +506,15 @@ class MlaPrefill:
     """Plan + workspace for one ragged prefill shape (batch, longest entry, H, longest sequence)."""
 
     def __init__(self, batch, max_q_len, num_heads, max_seq_len, dtype, device, split_kv=0, fold=0,
-                 kernel="auto", window=0):
+                 kernel="auto", window=0, sinks=0):
         self.plan = mla_prefill_plan(batch, max_q_len, num_heads, max_seq_len, dtype, split_kv, fold, kernel)
         if window:
             mla_decode_plan_window(self.plan, window)
+        if sinks:
+            mla_decode_plan_sinks(self.plan, sinks)
         self.device = torch.device(device)
         self.workspace = alloc_workspace(self.plan, self.device)
+        self._status = self.workspace[:4].view(torch.int32)  # the status word
         self.num_heads = num_heads
 
     def __call__(self, q, cu_seqlens_q, kv_cache, block_tables, seq_lens, softmax_scale, q_scale=1.0,
@@ -391,6 +527,13 @@ class MlaPrefill:
         mla_prefill(self.plan, q, cu_seqlens_q, kv_cache, block_tables, seq_lens, softmax_scale, out, lse,
                     self.workspace, q_scale, kv_scale, stream)
         return out, lse
+
+    def key_weights(self, q, cu_seqlens_q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, weights=None,
+                    decay=1.0, q_scale=1.0, kv_scale=1.0, stream=None):
+        """The weight every cached key received in the step that returned `lse` (see key_weights); device-side
+        problems show in status()."""
+        return key_weights(self.plan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, self._status,
+                           weights, decay, q_scale, kv_scale, cu_seqlens_q, stream=stream)
 
     def status(self, clear=True) -> int:
         return mla_decode_status(self.workspace, clear)

@@ -17,7 +17,6 @@ int cuda_failure(cudaError_t e) {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 
 int check_device_arch() {
   static std::mutex mu;
@@ -80,7 +79,7 @@ int check_plan(const mla_plan* p) {
     return MLA_ERR_PLAN_MISMATCH;
   if (p->kernel == MLA_KERNEL_TCGEN05_SOLO && p->dtype != MLA_FP8_E4M3) return MLA_ERR_PLAN_MISMATCH;
   if (p->schedule != MLA_SCHEDULE_SPLITS && p->schedule != MLA_SCHEDULE_BALANCED) return MLA_ERR_PLAN_MISMATCH;
-  if (p->window < 0) return MLA_ERR_PLAN_MISMATCH;
+  if (p->window < 0 || p->sinks < 0) return MLA_ERR_PLAN_MISMATCH;
   // the failure-detection test modes exist on the FP8 CTA-pair kernel only;
   // mode 2 (stores past the buffers, caught by the checks) in the checking
   // build only
@@ -211,7 +210,11 @@ int run_partial(const DecodeArgs& a, cudaStream_t st) {
   }
   if (a.plan.batch == 0 || a.total_q == 0) return MLA_OK;
   cudaError_t e;
-  if (a.plan.kernel == MLA_KERNEL_SIMT)
+  if (a.plan.schedule == MLA_SCHEDULE_BALANCED && a.plan.window > 0 && a.plan.sinks > 0) {
+    DecodeArgs whole = a;  // the plain kernel, every unit in one piece
+    whole.plan.split_kv = 1;
+    e = launch_simt_partial(whole, st);
+  } else if (a.plan.kernel == MLA_KERNEL_SIMT)
     e = launch_simt_partial(a, st);
   else if (a.plan.kernel == MLA_KERNEL_TCGEN05_SOLO)
     e = launch_tc_fp8_partial(a, st);
@@ -225,6 +228,7 @@ int run_partial(const DecodeArgs& a, cudaStream_t st) {
 int run_combine(const DecodeArgs& a, cudaStream_t st) {
   if (a.plan.batch == 0 || a.total_q == 0) return MLA_OK;
   if (a.plan.schedule == MLA_SCHEDULE_BALANCED) {
+    if (a.plan.window > 0 && a.plan.sinks > 0) return MLA_OK;
     const cudaError_t e = launch_combine_balanced(a, st);
     return e == cudaSuccess ? MLA_OK : cuda_failure(e);
   }
@@ -409,4 +413,145 @@ extern "C" int mla_decode_plan_window(mla_plan* plan, int window) {
     return MLA_ERR_UNSUPPORTED_SHAPE;
   plan->window = window;
   return MLA_OK;
+}
+
+extern "C" int mla_decode_plan_sinks(mla_plan* plan, int sinks) {
+  if (!plan || sinks < 0) return MLA_ERR_INVALID_ARG;
+  mla_plan p = *plan;
+  p.sinks = 0;
+  if (int rc = check_plan(&p); rc != MLA_OK) return rc;
+  if (sinks > 0 && !(p.kernel == MLA_KERNEL_SIMT ||
+                     (p.kernel == MLA_KERNEL_TCGEN05 && p.schedule == MLA_SCHEDULE_BALANCED)))
+    return MLA_ERR_UNSUPPORTED_SHAPE;
+  plan->sinks = sinks;
+  return MLA_OK;
+}
+
+extern "C" int mla_key_weights(const mla_plan* plan, const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                               const void* kv_cache, int64_t num_pages, int page_size, const int32_t* block_tables,
+                               int max_pages_per_seq, const int32_t* seq_lens, float softmax_scale, float q_scale,
+                               float kv_scale, const float* lse, const float* weights_in, int64_t in_stride,
+                               float decay, float* weights_out, int64_t out_stride, int64_t cols,
+                               int32_t* device_status, void* stream) {
+  if (int rc = check_plan(plan); rc != MLA_OK) return rc;
+  const mla_plan& p = *plan;
+  if (p.varlen && !cu_seqlens_q) return MLA_ERR_INVALID_ARG;
+  if ((cu_seqlens_q != nullptr) != (p.varlen != 0)) return MLA_ERR_PLAN_MISMATCH;
+  if (!p.varlen) total_q = (int64_t)p.batch * p.q_len;
+  if (total_q < 0 || total_q > (int64_t)p.batch * p.q_len) return MLA_ERR_INVALID_ARG;
+  if (page_size != MLA_PAGE_SIZE) return MLA_ERR_UNSUPPORTED_SHAPE;
+  const bool fp8 = p.dtype == MLA_FP8_E4M3;
+  if (!std::isfinite(softmax_scale) || !std::isfinite(decay) || decay < 0.f) return MLA_ERR_INVALID_ARG;
+  if (fp8 && (!std::isfinite(q_scale) || !std::isfinite(kv_scale) || q_scale <= 0.f || kv_scale <= 0.f))
+    return MLA_ERR_INVALID_ARG;
+  if (!device_status || !aligned(device_status, 4)) return MLA_ERR_INVALID_ARG;
+  if (p.batch == 0) return MLA_OK;
+  if (!kv_cache || !block_tables || !seq_lens || !weights_out) return MLA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!q || !lse)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4) || !aligned(cu_seqlens_q, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (num_pages > (int64_t(1) << 31) / MLA_PAGE_SIZE) return MLA_ERR_UNSUPPORTED_SHAPE;
+  const int64_t table_keys = (int64_t)max_pages_per_seq * MLA_PAGE_SIZE;
+  if (cols < (p.max_seq_len < table_keys ? p.max_seq_len : table_keys) || out_stride < cols ||
+      (weights_in && in_stride < cols))
+    return MLA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_failure(e);
+  if ((total_q > 0 && (!device_addressable(q, dev) || !device_addressable(lse, dev))) ||
+      !device_addressable(kv_cache, dev) || !device_addressable(block_tables, dev) ||
+      !device_addressable(seq_lens, dev) || !device_addressable(weights_out, dev) ||
+      !device_addressable(device_status, dev) || (weights_in && !device_addressable(weights_in, dev)) ||
+      (cu_seqlens_q && !device_addressable(cu_seqlens_q, dev)))
+    return MLA_ERR_INVALID_ARG;
+  if (int rc = check_device_arch(); rc != MLA_OK) return rc;
+  KeyWeightArgs k{};
+  k.a.plan = p;
+  k.a.q = q;
+  k.a.kv_cache = kv_cache;
+  k.a.num_pages = num_pages;
+  k.a.block_tables = block_tables;
+  k.a.max_pages_per_seq = max_pages_per_seq;
+  k.a.seq_lens = seq_lens;
+  k.a.score_scale_log2 =
+      (float)((double)softmax_scale * (fp8 ? (double)q_scale * kv_scale : 1.0) * (double)kLog2e);
+  k.a.status = device_status;
+  k.a.cu_q = cu_seqlens_q;
+  k.a.total_q = total_q;
+  k.lse = lse;
+  k.w_in = decay != 0.f ? weights_in : nullptr;
+  k.in_stride = in_stride;
+  k.decay = decay;
+  k.w_out = weights_out;
+  k.out_stride = out_stride;
+  k.cols = cols;
+  const cudaError_t e = launch_key_weights_simt(k, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_failure(e);
+}
+
+extern "C" int mla_cache_evict(const float* weights, int64_t weights_stride, int64_t cols, const int32_t* seq_lens,
+                               int batch, int budget, int sinks, int recent, const void* kv_cache, int64_t num_pages,
+                               int page_size, const int32_t* block_tables, int max_pages_per_seq, void* out_cache,
+                               int64_t out_num_pages, const int32_t* out_block_tables, int out_max_pages_per_seq,
+                               int dtype, int32_t* out_seq_lens, int32_t* kept, float* out_weights,
+                               int64_t out_weights_stride, int32_t* device_status, void* stream) {
+  if (batch < 0 || budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return MLA_ERR_INVALID_ARG;
+  if (page_size != MLA_PAGE_SIZE) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (dtype != MLA_BF16 && dtype != MLA_FP16 && dtype != MLA_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!weights || !seq_lens || !kv_cache || !block_tables || !out_cache || !out_block_tables || !out_seq_lens || !kept)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(kv_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(out_cache, 16) || !aligned(out_block_tables, 4) || !aligned(out_seq_lens, 4) || !aligned(kept, 4) ||
+      !aligned(out_weights, 4) || !aligned(device_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (num_pages < 1 || out_num_pages < 1 || max_pages_per_seq < 1 || cols < 1 || weights_stride < cols ||
+      (out_weights && out_weights_stride < budget) || (int64_t)out_max_pages_per_seq * MLA_PAGE_SIZE < budget)
+    return MLA_ERR_INVALID_ARG;
+  if (num_pages > (int64_t(1) << 40) / MLA_PAGE_SIZE || out_num_pages > (int64_t(1) << 40) / MLA_PAGE_SIZE)
+    return MLA_ERR_UNSUPPORTED_SHAPE;
+  // A result on the pages it is gathered from, or new weights over the old,
+  // would overwrite what is still to be read.
+  if (kv_cache == out_cache && block_tables == out_block_tables) return MLA_ERR_INVALID_ARG;
+  if (out_weights) {
+    const float* w_end = weights + (int64_t)(batch - 1) * weights_stride + cols;
+    const float* o_end = out_weights + (int64_t)(batch - 1) * out_weights_stride + budget;
+    if (out_weights < w_end && weights < o_end) return MLA_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_failure(e);
+  if (!device_addressable(weights, dev) || !device_addressable(seq_lens, dev) || !device_addressable(kv_cache, dev) ||
+      !device_addressable(block_tables, dev) || !device_addressable(out_cache, dev) ||
+      !device_addressable(out_block_tables, dev) || !device_addressable(out_seq_lens, dev) ||
+      !device_addressable(kept, dev) || (out_weights && !device_addressable(out_weights, dev)) ||
+      (device_status && !device_addressable(device_status, dev)))
+    return MLA_ERR_INVALID_ARG;
+  if (int rc = check_device_arch(); rc != MLA_OK) return rc;
+  EvictArgs e{};
+  e.weights = weights;
+  e.weights_stride = weights_stride;
+  e.cols = cols;
+  e.seq_lens = seq_lens;
+  e.batch = batch;
+  e.budget = budget;
+  e.sinks = sinks;
+  e.recent = recent;
+  e.kv_cache = static_cast<const uint8_t*>(kv_cache);
+  e.num_pages = num_pages;
+  e.block_tables = block_tables;
+  e.max_pages_per_seq = max_pages_per_seq;
+  e.out_cache = static_cast<uint8_t*>(out_cache);
+  e.out_num_pages = out_num_pages;
+  e.out_block_tables = out_block_tables;
+  e.out_max_pages_per_seq = out_max_pages_per_seq;
+  e.row_bytes = MLA_D_QK * (dtype == MLA_FP8_E4M3 ? 1 : 2);
+  e.out_seq_lens = out_seq_lens;
+  e.kept = kept;
+  e.out_weights = out_weights;
+  e.out_weights_stride = out_weights_stride;
+  e.status = device_status;
+  const cudaError_t rc = launch_cache_evict(e, reinterpret_cast<cudaStream_t>(stream));
+  return rc == cudaSuccess ? MLA_OK : cuda_failure(rc);
 }

@@ -120,6 +120,9 @@ __device__ __forceinline__ UnitGeom unit_geom(const DecodeArgs& a, int u, bool f
   ug.klo = (tu > 0 && p.window > 0) ? max(0, ug.nq + 1 - p.window) : 0;
   return ug;
 }
+// Whether the plan keeps its first keys visible beside a window (sinks without
+// a window change nothing).
+__host__ __device__ __forceinline__ bool plan_has_sinks(const mla_plan& p) { return p.window > 0 && p.sinks > 0; }
 // First key of the row whose last key is `last` (its sliding window's start).
 __device__ __forceinline__ int row_key_lo(const mla_plan& p, int last) {
   return p.window > 0 ? max(0, last + 1 - p.window) : 0;

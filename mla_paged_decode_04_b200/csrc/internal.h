@@ -17,6 +17,7 @@ namespace mla {
 
 constexpr uint32_t kPlanMagic = 0x4d4c4131u;  // "MLA1"
 constexpr int kNumSMs = 148;                    // B200
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHeaderBytes = 256;               // workspace header (status word at offset 0)
 constexpr int kTileKeys = 64;                   // keys per tile = one cache page
 constexpr int kPairTileKeys = 128;              // keys per CTA-pair tile (one page per CTA)
@@ -91,6 +92,41 @@ struct DecodeArgs {
   int64_t total_q;         // query tokens in q (B * q_len for decode)
 };
 
+// One mla_key_weights call: the attention step it follows (out, workspace
+// fields unused), its LSE and the weights.
+struct KeyWeightArgs {
+  DecodeArgs a;
+  const float* lse;       // fp32 [total_q, H], natural log
+  const float* w_in;      // null: zeros
+  int64_t in_stride;
+  float decay;
+  float* w_out;
+  int64_t out_stride;
+  int64_t cols;
+};
+
+// One mla_cache_evict call.
+struct EvictArgs {
+  const float* weights;
+  int64_t weights_stride, cols;
+  const int32_t* seq_lens;
+  int batch, budget, sinks, recent;
+  const uint8_t* kv_cache;
+  int64_t num_pages;
+  const int32_t* block_tables;
+  int max_pages_per_seq;
+  uint8_t* out_cache;
+  int64_t out_num_pages;
+  const int32_t* out_block_tables;
+  int out_max_pages_per_seq;
+  int row_bytes;  // 576 or 1152
+  int32_t* out_seq_lens;
+  int32_t* kept;
+  float* out_weights;
+  int64_t out_weights_stride;
+  int32_t* status;  // may be null
+};
+
 // Pair of the balanced schedule whose range holds pair tile x (0 <= x < W):
 // pair p covers [floor(W p / np), floor(W (p + 1) / np)).
 __host__ __device__ inline int balanced_pair_of(int64_t x, int64_t W, int np) {
@@ -123,6 +159,8 @@ cudaError_t launch_kv_pack(const void* latent, const void* rope, int64_t n, cons
                            cudaStream_t stream);
 cudaError_t launch_kv_amax(const void* latent, const void* rope, int64_t n, int in_dtype, float* amax,
                            cudaStream_t stream);
+cudaError_t launch_key_weights_simt(const KeyWeightArgs& k, cudaStream_t stream);
+cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t stream);
 cudaError_t launch_combine_balanced(const DecodeArgs& a, cudaStream_t stream);
 // Zeroes `bytes` (a multiple of 16) at the 16-byte aligned `ws`, as a
 // programmatic dependent of the previous kernel in the stream (see combine.cu).

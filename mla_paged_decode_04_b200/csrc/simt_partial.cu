@@ -54,7 +54,11 @@ __global__ void __launch_bounds__(256) simt_partial_kernel(const DecodeArgs a) {
     float o[MLA_D_V / 32];
 #pragma unroll
     for (int i = 0; i < MLA_D_V / 32; ++i) o[i] = 0.f;
-    for (int j = max(key0, row_key_lo(p, last)); j < jend; ++j) {  // sliding window: the row's last keys
+    const int lo = row_key_lo(p, last);                   // sliding window: the row's last keys,
+    const int sk = plan_has_sinks(p) ? min(p.sinks, lo) : 0;  // and the sinks before it
+    for (int j = key0 < sk ? key0 : max(key0, lo); j < jend; ++j) {
+      if (j >= sk && j < lo) j = lo;  // from the last sink to the window
+      if (j >= jend) break;
       const int page = table[j / kTileKeys];
       if (page < 0 || (int64_t)page >= a.num_pages) {
         if (lane == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
