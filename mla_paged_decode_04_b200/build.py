@@ -92,7 +92,11 @@ def build(force: bool = False, verbose: bool = False, check: bool = False) -> st
             f.write(log)
         if verbose:
             print(log)
-        _check_spills(log, src)
+        try:
+            _check_spills(log, src)
+        except RuntimeError:
+            os.remove(obj)  # so that the next build looks at it again
+            raise
         changed = True
     if changed or os.path.getmtime(lib_path) < max(os.path.getmtime(o) for o in objs):
         tmp = lib_path + f".tmp{os.getpid()}"

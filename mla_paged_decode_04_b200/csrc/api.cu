@@ -210,11 +210,7 @@ int run_partial(const DecodeArgs& a, cudaStream_t st) {
   }
   if (a.plan.batch == 0 || a.total_q == 0) return MLA_OK;
   cudaError_t e;
-  if (a.plan.schedule == MLA_SCHEDULE_BALANCED && a.plan.window > 0 && a.plan.sinks > 0) {
-    DecodeArgs whole = a;  // the plain kernel, every unit in one piece
-    whole.plan.split_kv = 1;
-    e = launch_simt_partial(whole, st);
-  } else if (a.plan.kernel == MLA_KERNEL_SIMT)
+  if (a.plan.kernel == MLA_KERNEL_SIMT)
     e = launch_simt_partial(a, st);
   else if (a.plan.kernel == MLA_KERNEL_TCGEN05_SOLO)
     e = launch_tc_fp8_partial(a, st);
@@ -228,7 +224,6 @@ int run_partial(const DecodeArgs& a, cudaStream_t st) {
 int run_combine(const DecodeArgs& a, cudaStream_t st) {
   if (a.plan.batch == 0 || a.total_q == 0) return MLA_OK;
   if (a.plan.schedule == MLA_SCHEDULE_BALANCED) {
-    if (a.plan.window > 0 && a.plan.sinks > 0) return MLA_OK;
     const cudaError_t e = launch_combine_balanced(a, st);
     return e == cudaSuccess ? MLA_OK : cuda_failure(e);
   }

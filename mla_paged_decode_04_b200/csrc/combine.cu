@@ -150,7 +150,7 @@ __device__ __forceinline__ void combine_unit(const DecodeArgs& a, int u, int rb,
   // the first follows the unit's lead-in)
   const int lead = end > start ? unit_lead_weight(1) : 0;
   const int p0 = end > start ? balanced_pair_of(start + lead, W, np) : 0;
-  const int p1 = end > start ? balanced_pair_of(end - tile_weight(p, ug), W, np) : 0;
+  const int p1 = end > start ? balanced_pair_of(end - (plan_has_sinks(p) ? tile_weight<true>(p, ug) : tile_weight(p, ug)), W, np) : 0;
   if (end > start && p0 == p1) return;  // a whole unit: written by its pair
   // (block-uniform: every thread leaves together)
   if (end > start && !(in_bounds(a, 2 * p0 + 1, balanced_slots(a)) && in_bounds(a, 2 * p1, balanced_slots(a)))) return;

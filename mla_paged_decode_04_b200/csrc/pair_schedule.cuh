@@ -63,10 +63,40 @@ __device__ __forceinline__ int unit_min_keys(const mla_plan& p, const UnitGeom& 
 }
 
 // Weight of one tile of a unit: 3 when its rows' P goes as two E4M3 terms
-// (FP8 units whose first row sees fewer than kTwoTermKeys keys), else 2.
+// (FP8 units whose first row sees fewer than kTwoTermKeys keys; every FP8 unit
+// of a plan with sinks, so that the output's error does not depend on how long
+// a window a caller sets), else 2.
+template <bool kSinks = false>
 __device__ __forceinline__ int tile_weight(const mla_plan& p, const UnitGeom& ug) {
   if (p.dtype != MLA_FP8_E4M3) return 2;
+  if (kSinks) return 3;
   return unit_min_keys(p, ug) < kTwoTermKeys ? 3 : 2;
+}
+
+// Tiles of a unit under a window with sinks: those that hold the
+// first keys, then those from the window's first tile on; one run from tile 0
+// when the two meet. sink_tile() maps a unit's i-th tile to its place in the
+// sequence; it is computed again at each use, since the pair kernels have no
+// registers to spare for the map.
+template <int kKeys>
+__device__ __forceinline__ int sink_tile(const mla_plan& p, int klo, int i) {
+  const int nst = (min(p.sinks, klo) + kKeys - 1) / kKeys, tlo = klo / kKeys;
+  return (nst >= tlo || i < nst) ? i : i + tlo - nst;
+}
+template <int kKeys, bool kSinks>
+__device__ __forceinline__ int unit_tiles(const mla_plan& p, const UnitGeom& ug) {
+  const int t = unit_span_tiles<kKeys>(ug);
+  if (!kSinks || t == 0) return t;
+  const int nst = (min(p.sinks, ug.klo) + kKeys - 1) / kKeys;
+  return t + min(nst, ug.klo / kKeys);  // (the tiles from 0 on where the two meet)
+}
+// Whether some row of the unit sees a key of the page at `key` (a multiple of
+// 64), and whether every key of it is seen by some row.
+__device__ __forceinline__ bool page_seen(int key, int klo, int kend, int sinks) {
+  return key < kend && (key + kTileKeys > klo || key < sinks);
+}
+__device__ __forceinline__ bool page_all_seen(int key, int klo, int kend, int sinks) {
+  return key + kTileKeys <= kend && (key >= klo || key + kTileKeys <= sinks);
 }
 
 // Tiles [i0, i1) of a unit with `t` tiles of weight `w` starting at weighted
@@ -106,7 +136,7 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
 // memory and, when there are more, all of them to this CTA's part of the
 // spill area (read back by load_piece). CTA 0 of pair 0 also writes the slot
 // start table the combine reads, then its ready flag.
-template <int kKeys>
+template <int kKeys, bool kSinks = false>
 __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uint8_t* sched_area) {
   const mla_plan& p = a.plan;
   Piece* smem_list = reinterpret_cast<Piece*>(sched_area);
@@ -128,13 +158,13 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
       return;
     }
     const UnitGeom ug = unit_geom(a, sched_unit(p, sl), false);
-    t = unit_span_tiles<kKeys>(ug), w = tile_weight(p, ug);
+    t = unit_tiles<kKeys, kSinks>(p, ug), w = tile_weight<kSinks>(p, ug);
   };
   // scan 1: the weighted start of this thread's run
   int run = 0;
   for (int sl = s_beg; sl < s_end; ++sl) {
     const UnitGeom ug = unit_geom(a, sched_unit(p, sl), writer);
-    const int t = unit_span_tiles<kKeys>(ug), w = tile_weight(p, ug);
+    const int t = unit_tiles<kKeys, kSinks>(p, ug), w = tile_weight<kSinks>(p, ug);
     if (sl == s_beg) t_beg = t, w_beg = w;
     run += unit_lead_weight(t) + t * w;
   }

@@ -87,7 +87,8 @@ struct Layout16 {
   static constexpr int B_QK_DONE = B_FIN + 1;
   static constexpr int B_EPI = B_QK_DONE + NQ;       // local, per piece: the output tile is staged
   static constexpr int B_O_FREE = B_EPI + 1;         // leader, per piece: both CTAs read O
-  static constexpr int kNBars = B_O_FREE + 1;
+  static constexpr int B_V_LAND = B_O_FREE + 1;      // local, + V slot (sinks): this CTA's V landed
+  static constexpr int kNBars = B_V_LAND + NV;
   static_assert(8 * kNBars <= 512, "barrier area");
   static constexpr uint32_t kMiscOff = kBarOff + 512;
   // The dynamic shared memory base is 1024-aligned (checked at run time;
@@ -124,11 +125,25 @@ struct PieceCtx16 {
   const int32_t* table;
   bool whole;  // the piece is the whole unit: final output, not a partial
   bool cont;   // the piece begins inside its unit (the pair's first piece)
+  int klo;  // with sinks: the window's first key (key1: the unit's end)
+  int t0;   // first tile of the piece within its unit
 #if MLA_BOUNDS_CHECK
   bool table_ok;  // the piece's block-table entries lie inside row b of the table
 #endif
 };
 
+// Place in the sequence of the piece's tile j (sinks).
+__device__ __forceinline__ int piece_tile(const mla_plan& p, const PieceCtx16& c, int j) {
+  return sink_tile<kTile16>(p, c.klo, c.t0 + j);
+}
+
+// Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
+// V rows of a tile that no row of the unit sees (past the sequence's end, or
+// between the sinks and the window) are zeroed in shared memory before the
+// P.V. The loads of such a tile signal a barrier of their own CTA instead of
+// the leader's V_FULL; the softmax group that writes the tile's P waits for it,
+// clears the rows and hands both over with P_FULL.
+template <bool kSinks>
 __device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const Piece& pc) {
   PieceCtx16 c;
   const UnitGeom ug = unit_geom(a, pc.u, false);
@@ -146,27 +161,36 @@ __device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const Pie
   c.table = a.block_tables + (int64_t)c.b * a.max_pages_per_seq;
   c.whole = pc.t0 == 0 && c.key1 >= ug.kend;
   c.cont = pc.t0 > 0;
+  c.klo = ug.klo;
+  c.t0 = pc.t0;
+  if constexpr (kSinks) {
+    c.key1 = ug.kend;
+    c.whole = pc.t0 == 0 && pc.t1 == unit_tiles<kTile16, true>(a.plan, ug);
+  }
 #if MLA_BOUNDS_CHECK
-  c.table_ok = c.n_pt <= 0 || (in_bounds(a, c.b, a.plan.batch) && in_bounds(a, c.page0, a.max_pages_per_seq) &&
-                               in_bounds(a, (int64_t)c.page0 + c.n_pt - 1, a.max_pages_per_seq));
+  c.table_ok = c.n_pt <= 0 || (in_bounds(a, c.b, a.plan.batch) &&
+                               in_bounds(a, kSinks ? piece_tile(a.plan, c, 0) : c.page0, a.max_pages_per_seq) &&
+                               in_bounds(a, kSinks ? piece_tile(a.plan, c, c.n_pt - 1) : (int64_t)c.page0 + c.n_pt - 1,
+                                         a.max_pages_per_seq));
 #endif
   return c;
 }
 
 // Block-table entry of pair tile j of the piece, read one tile ahead of its
 // use with a load kept ahead of the next barrier wait.
-__device__ __forceinline__ int piece_entry16(const PieceCtx16& c, int j) {
+template <bool kSinks>
+__device__ __forceinline__ int piece_entry16(const mla_plan& p, const PieceCtx16& c, int j) {
 #if MLA_BOUNDS_CHECK
   if (!c.table_ok) return 0;  // outputs unspecified: MLA_DEV_BOUNDS is set
 #endif
-  return j < c.n_pt ? ld_nc_ordered(c.table + c.page0 + j) : 0;
+  return j < c.n_pt ? ld_nc_ordered(c.table + (kSinks ? piece_tile(p, c, j) : c.page0 + j)) : 0;
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page16(const DecodeArgs& a, int pg) {
   return (pg < 0 || (int64_t)pg >= a.num_pages) ? 0 : pg;
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kSinks>
 __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* smem, int npc,
                                            int n_all) {
   using L = Layout16;
@@ -202,7 +226,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx16 c = piece_ctx16(a, load_piece(a, smem, k));
+        const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
         if (k > 0) {
           // the Q areas and the staging slots are free once every MMA of the
           // previous piece is done: its O_FINAL phase
@@ -216,11 +240,11 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           tma_load_2d(sb + L::kQRes + ci * 8192, &prm.tm_q, 256 + 64 * ci, qrow, bar(L::B_Q_MAIN), pol_q);
         }
         tma_load_2d(sb + L::kQRopeStage, &prm.tm_q, 512, qrow, bar(L::B_Q_MAIN), pol_q);
-        int entry_nx = piece_entry16(c, 0);
+        int entry_nx = piece_entry16<kSinks>(p, c, 0);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sk = jt % NK;
           const int page = valid_page16(a, entry_nx);
-          if (j + 1 < c.n_pt) entry_nx = piece_entry16(c, j + 1);
+          if (j + 1 < c.n_pt) entry_nx = piece_entry16<kSinks>(p, c, j + 1);
           if (!(ok = bounded_wait_cta(bar(L::B_K_EMPTY + sk), ((jt / NK) & 1) ^ 1, abort_flag, a.status))) break;
           const uint32_t ks = sb + L::kKOff + sk * L::kKSlot;
           const uint32_t full = lead(L::B_K_FULL + sk);
@@ -242,18 +266,25 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx16 c = piece_ctx16(a, load_piece(a, smem, k));
-        int e_nx = piece_entry16(c, 0);
+        const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
+        int e_nx = piece_entry16<kSinks>(p, c, 0);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sv = jt % NV;
           const int pg = valid_page16(a, e_nx);
-          if (j + 1 < c.n_pt) e_nx = piece_entry16(c, j + 1);
+          if (j + 1 < c.n_pt) e_nx = piece_entry16<kSinks>(p, c, j + 1);
           // the scores of the tile exist: its page is in L2 now
           if (!(ok = bounded_wait_cta(bar(L::B_QK_DONE + jt % NQ), (jt / NQ) & 1, abort_flag, a.status))) break;
           if (!(ok = bounded_wait_cta(bar(L::B_V_EMPTY + sv), ((jt / NV) & 1) ^ 1, abort_flag, a.status))) break;
           const uint32_t vs = sb + L::kVOff + sv * L::kVSlot;
-          const uint32_t full = lead(L::B_V_FULL + sv);
-          if (rank == 0) mbar_arrive_expect_tx(bar(L::B_V_FULL + sv), 2u * L::kVSlot);
+          uint32_t full = lead(L::B_V_FULL + sv);
+          if (kSinks && !page_all_seen(kTile16 * piece_tile(p, c, j), c.klo, c.key1, p.sinks)) {
+            if (rank == 0) mbar_arrive(bar(L::B_V_FULL + sv));
+            full = mapa(bar(L::B_V_LAND + sv), rank);
+            mbar_arrive_expect_tx(bar(L::B_V_LAND + sv), L::kVSlot);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(bar(L::B_V_FULL + sv), 2u * L::kVSlot);
+            if (kSinks) mbar_arrive(bar(L::B_V_LAND + sv));
+          }
           // half h: this CTA's V columns [256h + 128 rank, +128), two chunks
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -261,6 +292,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
         }
       }
       if (rank == 0) drain_loads(bar(L::B_V_FULL), NV, n_all);
+      if (kSinks) drain_loads(bar(L::B_V_LAND), NV, n_all);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q.K^T issuer (leader)
@@ -364,7 +396,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
     int jt = 0;  // running index of the piece's first tile
 
     for (int k = 0; ok && k < npc; ++k) {
-      const PieceCtx16 c = piece_ctx16(a, load_piece(a, smem, k));
+      const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
       const bool last_piece = k == npc - 1;
       // causal limit and sliding-window start of this row (rows past the
       // unit compute on whatever Q holds and are never stored)
@@ -407,13 +439,13 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
       float m_grp = -INFINITY, l_grp = 0.f;  // this group's reference and partial sum (this half row)
       float m_last = -INFINITY;              // the reference of this group's previous tile of the piece
       const int j_first = (jt & 1) == grp ? 0 : 1;
-      int pg_next = j_first < c.n_pt ? piece_entry16(c, j_first) : 0;
+      int pg_next = j_first < c.n_pt ? piece_entry16<kSinks>(p, c, j_first) : 0;
       for (int j = j_first; ok && j < c.n_pt; j += 2) {
         const int jg = jt + j;   // running tile index
         const int buf = jg & 1;  // == grp
         const int ph = (jg >> 1) & 1;
         const int pg_cur = pg_next;
-        if (j + 2 < c.n_pt) pg_next = piece_entry16(c, j + 2);
+        if (j + 2 < c.n_pt) pg_next = piece_entry16<kSinks>(p, c, j + 2);
         if (!(ok = warp_wait_cta(bar(L::B_S_FULL + buf), ph, abort_flag, a.status))) break;
         tc_fence_after();
         uint32_t sv[32];
@@ -428,12 +460,13 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           page_ok = false;
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
-        const int kb = c.key0 + kTile16 * j + kHalfKeys * hf;
+        const int kb = (kSinks ? kTile16 * piece_tile(p, c, j) : c.key0 + kTile16 * j) + kHalfKeys * hf;
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
-        if (!(page_ok && kb >= lower && kb + 31 <= limit)) {
+        if (!(page_ok && (kb >= lower || (kSinks && kb + 31 < p.sinks)) && kb + 31 <= limit)) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!(page_ok && kb + i >= lower && kb + i <= limit)) sv[i] = __float_as_uint(-INFINITY);
+            if (!(page_ok && (kb + i >= lower || (kSinks && kb + i < p.sinks)) && kb + i <= limit))
+              sv[i] = __float_as_uint(-INFINITY);
         }
         float mt;
         {
@@ -555,6 +588,21 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
             tmem_st32(tmem + tl + kOCol + 32u * (cc + 1), o1);
           }
           tmem_wait_st();
+        }
+        if constexpr (kSinks) {
+          const int kp = kTile16 * piece_tile(p, c, j);
+          if (!page_all_seen(kp, c.klo, c.key1, p.sinks)) {
+            const int sv_slot = jg % NV;
+            if (!(ok = warp_wait_cta(bar(L::B_V_LAND + sv_slot), (jg / NV) & 1, abort_flag, a.status))) break;
+            // one (key, column half) per thread of the group
+            const int key = threadIdx.x & 63, h2 = (threadIdx.x >> 6) & 1;
+            if (kp + key >= c.key1 || (kp + key < c.klo && kp + key >= p.sinks)) {
+              uint8_t* vrow = smem + L::kVOff + sv_slot * L::kVSlot + h2 * 16384 + key * 128;
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                *reinterpret_cast<uint4*>(vrow + (u >> 3) * 8192 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -771,6 +819,7 @@ __device__ __forceinline__ void pair_setup16(const Pair16Params& prm, uint8_t* s
     for (int i = 0; i < NV; ++i) {
       mbar_init(bar(L::B_V_FULL + i), 1);
       mbar_init(bar(L::B_V_EMPTY + i), 1);
+      mbar_init(bar(L::B_V_LAND + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::B_S_FULL + i), 1);
@@ -823,6 +872,7 @@ __device__ __forceinline__ void pair_idle_teardown16(uint8_t* smem) {
   }
 }
 
+template <bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc16_pair_kernel(const __grid_constant__ Pair16Params prm) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -845,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The combine grid may now start (the unit counters and the table's ready
   // flag it waits on are cleared) and take the SMs of pairs that finish early.
   launch_dependents();
-  build_schedule<kTile16>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
+  build_schedule<kTile16, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
   __syncthreads();
   const int npc = info->npc;
   if (npc == 0) {  // no work for this pair (the same in both CTAs)
@@ -858,9 +908,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     discard_pair_slots(prm.a, blockIdx.x >> 1, cluster_ctarank(), info->tiles, threadIdx.x - 32 * kSoftmaxWarp0,
                        kThreads - 32 * kSoftmaxWarp0);
   if (prm.a.plan.dtype == MLA_BF16)
-    pair_cta16<true>(prm, smem, npc, info->tiles);
+    pair_cta16<true, kSinks>(prm, smem, npc, info->tiles);
   else
-    pair_cta16<false>(prm, smem, npc, info->tiles);
+    pair_cta16<false, kSinks>(prm, smem, npc, info->tiles);
 }
 
 }  // namespace
@@ -880,8 +930,10 @@ cudaError_t launch_tc16_pair_partial(const DecodeArgs& a, cudaStream_t stream) {
       !encode_rows_576_chunks(&prm.tm_v[0], kv, 2, kv_rows, 6, 128, kTile16, 2) ||
       !encode_rows_576_chunks(&prm.tm_v[1], kv + 256, 2, kv_rows, 6, 128, kTile16, 2))
     return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> smem_set{0};
-  if (cudaError_t e = set_max_dynamic_smem((const void*)tc16_pair_kernel, (int)Layout16::kSmemBytes, smem_set);
+  static std::atomic<uint64_t> smem_set[2];
+  const bool sinks = plan_has_sinks(p);
+  auto* const kernel = sinks ? tc16_pair_kernel<true> : tc16_pair_kernel<false>;
+  if (cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)Layout16::kSmemBytes, smem_set[sinks]);
       e != cudaSuccess)
     return e;
   // a programmatic dependent of the previous kernel in the stream (the
@@ -896,7 +948,7 @@ cudaError_t launch_tc16_pair_partial(const DecodeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tc16_pair_kernel, prm);
+  return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
 }  // namespace mla

@@ -133,7 +133,8 @@ struct PairLayout {
   static constexpr int B_QK_DONE = B_FIN + 1;
   static constexpr int B_EPI = B_QK_DONE + NQ;       // local, per piece: the output tile is staged
   static constexpr int B_O_FREE = B_EPI + 1;         // leader, per piece: both CTAs read O
-  static constexpr int kNBars = B_O_FREE + 1;
+  static constexpr int B_V_LAND = B_O_FREE + 1;      // local, + V slot (sinks): this CTA's V landed
+  static constexpr int kNBars = B_V_LAND + NV;
   static_assert(8 * kNBars <= 512, "barrier area");
   static constexpr uint32_t kSmemBytes = kFinOff + 2048 + 1024;  // + alignment slack of the base
   static_assert(kPOff % 1024 == 0 && kKOff % 1024 == 0 && kKSlot % 1024 == 0 && kVOff % 1024 == 0, "alignment");
@@ -170,6 +171,8 @@ struct PieceCtx {
   bool whole;  // the piece is the whole unit: final output, not a partial
   bool cont;   // the piece begins inside its unit (the pair's first piece)
   bool two;    // two-term P
+  int klo;  // with sinks: the window's first key (key1: the unit's end)
+  int t0;   // first tile of the piece within its unit
 };
 
 // The unit geometry as a call, not inlined into every role: the roles' code
@@ -178,6 +181,18 @@ struct PieceCtx {
 // faster with it inlined).
 __device__ __noinline__ UnitGeom unit_geom_call(const DecodeArgs& a, int u) { return unit_geom(a, u, false); }
 
+// Place in the sequence of the piece's tile j (sinks).
+__device__ __forceinline__ int piece_tile(const mla_plan& p, const PieceCtx& c, int j) {
+  return sink_tile<kPairTileKeys>(p, c.klo, c.t0 + j);
+}
+
+// Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
+// V rows of a tile that no row of the unit sees (past the sequence's end, or
+// between the sinks and the window) are zeroed in shared memory before the
+// P.V. The loads of such a tile signal a barrier of their own CTA instead of
+// the leader's V_FULL; the softmax group that writes the tile's P waits for it,
+// clears the rows and hands both over with P_FULL.
+template <bool kSinks>
 __device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& pc, bool kTwo) {
   const mla_plan& p = a.plan;
   PieceCtx c;
@@ -198,7 +213,14 @@ __device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& 
   c.table = a.block_tables + (int64_t)c.b * a.max_pages_per_seq;
   c.whole = pc.t0 == 0 && c.key1 >= ug.kend;
   c.cont = pc.t0 > 0;
-  c.two = kTwo && tile_weight(p, ug) == 3;  // the same rule as the schedule's weights
+  c.two = kTwo && tile_weight<kSinks>(p, ug) == 3;  // the same rule as the schedule's weights
+  c.klo = ug.klo;
+  c.t0 = pc.t0;
+  if constexpr (kSinks) {
+    c.key1 = ug.kend;
+    c.whole = pc.t0 == 0 && pc.t1 == unit_tiles<kPairTileKeys, true>(p, ug);
+    return c;
+  }
 #if MLA_BOUNDS_CHECK
   // the piece's block-table entries [tile0, tile0 + n_tiles) of row b; if any
   // lies outside, none is read and every key of the piece is masked
@@ -212,15 +234,31 @@ __device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& 
 // Block-table entry of 64-key tile t of the piece (0 past its end), read one
 // tile ahead of its use: the load is issued before the next barrier wait and
 // checked after it, so its latency stays off the ring's critical path.
-__device__ __forceinline__ int piece_entry(const PieceCtx& c, int t) {
+template <bool kSinks>
+__device__ __forceinline__ int piece_entry(const DecodeArgs& a, const PieceCtx& c, int t) {
+  const mla_plan& p = a.plan;
+  if constexpr (kSinks) {
+    // a page that no row sees is not looked up (its V rows are cleared)
+    const int page = 2 * piece_tile(p, c, t >> 1) + (t & 1);
+    if (t >= 2 * c.n_pt || !page_seen(kTileKeys * page, c.klo, c.key1, p.sinks)) return 0;
+#if MLA_BOUNDS_CHECK
+    if (!in_bounds(a, c.b, p.batch) || !in_bounds(a, page, a.max_pages_per_seq)) return 0;
+#endif
+    return ld_nc_ordered(c.table + page);
+  }
   return t < c.n_tiles ? ld_nc_ordered(c.table + c.tile0 + t) : 0;
+}
+// Whether every key of pair tile j of the piece is seen by some row (sinks).
+__device__ __forceinline__ bool tile_all_seen(const mla_plan& p, const PieceCtx& c, int j) {
+  const int key = kPairTileKeys * piece_tile(p, c, j);
+  return page_all_seen(key, c.klo, c.key1, p.sinks) && page_all_seen(key + kTileKeys, c.klo, c.key1, p.sinks);
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page(const DecodeArgs& a, int pg) {
   return (pg < 0 || (int64_t)pg >= a.num_pages) ? 0 : pg;
 }
 
-template <bool kTwo>
+template <bool kTwo, bool kSinks>
 __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, int npc,
                                          int n_all) {
   using L = PairLayout<kTwo>;
@@ -264,7 +302,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;     // tile counter across pieces
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx(a, load_piece(a, smem, k), kTwo);
+        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
         if (k > 0) {
           // Q rope, Q in TMEM and the staging slot are free once every MMA of
           // the previous piece is done: its O_FINAL phase. (The V ring's own
@@ -279,11 +317,11 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
           tma_load_2d(sb + L::kQStage + ci * 8192, &prm.tm_q_main, 128 * ci, qrow, bar(L::B_Q_MAIN), pol_q);
         if (rank == 0) mbar_arrive_expect_tx(bar(L::B_Q_ROPE), 2u * 64u * (uint32_t)box_q);
         tma_load_2d_pair(sb + L::kQRope, &prm.tm_q_rope, 512, qrow, lead(L::B_Q_ROPE), pol_q);
-        int entry_nx = piece_entry(c, (int)rank);
+        int entry_nx = piece_entry<kSinks>(a, c, (int)rank);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sk = jt % NK;
           const int page = valid_page(a, entry_nx);
-          if (j + 1 < c.n_pt) entry_nx = piece_entry(c, 2 * (j + 1) + (int)rank);
+          if (j + 1 < c.n_pt) entry_nx = piece_entry<kSinks>(a, c, 2 * (j + 1) + (int)rank);
           if (!(ok = bounded_wait_cta(bar(L::B_K_EMPTY + sk), ((jt / NK) & 1) ^ 1, abort_flag, a.status))) break;
           // failure-detection test mode: the pair's first tile is never loaded,
           // so the S issuer's wait for it runs out (every wait is bounded)
@@ -309,21 +347,28 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx(a, load_piece(a, smem, k), kTwo);
-        int e0_nx = piece_entry(c, 0), e1_nx = piece_entry(c, 1);
+        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+        int e0_nx = piece_entry<kSinks>(a, c, 0), e1_nx = piece_entry<kSinks>(a, c, 1);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sv = jt % NV;
           const int pg0 = valid_page(a, e0_nx), pg1 = valid_page(a, e1_nx);
           if (j + 1 < c.n_pt) {
-            e0_nx = piece_entry(c, 2 * (j + 1));
-            e1_nx = piece_entry(c, 2 * (j + 1) + 1);
+            e0_nx = piece_entry<kSinks>(a, c, 2 * (j + 1));
+            e1_nx = piece_entry<kSinks>(a, c, 2 * (j + 1) + 1);
           }
           // the scores of the tile exist: its pages are in L2 now
           if (!(ok = bounded_wait_cta(bar(L::B_QK_DONE + jt % NQ), (jt / NQ) & 1, abort_flag, a.status))) break;
           if (!(ok = bounded_wait_cta(bar(L::B_V_EMPTY + sv), ((jt / NV) & 1) ^ 1, abort_flag, a.status))) break;
           const uint32_t vs = sb + L::kVOff + sv * L::kVSlot;
-          const uint32_t full = lead(L::B_V_FULL + sv);
-          if (rank == 0) mbar_arrive_expect_tx(bar(L::B_V_FULL + sv), 2u * L::kVSlot);
+          uint32_t full = lead(L::B_V_FULL + sv);
+          if (kSinks && !tile_all_seen(p, c, j)) {
+            if (rank == 0) mbar_arrive(bar(L::B_V_FULL + sv));
+            full = mapa(bar(L::B_V_LAND + sv), rank);
+            mbar_arrive_expect_tx(bar(L::B_V_LAND + sv), L::kVSlot);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(bar(L::B_V_FULL + sv), 2u * L::kVSlot);
+            if (kSinks) mbar_arrive(bar(L::B_V_LAND + sv));
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int x = 128 * (2 * h + (int)rank);  // this CTA's 128 of the 256 columns of half h
@@ -333,6 +378,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
         }
       }
       if (rank == 0) drain_loads(bar(L::B_V_FULL), NV, n_all);
+      if (kSinks) drain_loads(bar(L::B_V_LAND), NV, n_all);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q.K^T issuer (leader)
@@ -379,7 +425,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx(a, load_piece(a, smem, k), kTwo);
+        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
         // the piece's first P.V overwrites O: the previous piece's epilogue
         // must have read it
         if (k > 0 && !(ok = warp_wait(bar(L::B_O_FREE), (k - 1) & 1, abort_flag, a.status))) break;
@@ -431,7 +477,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
     int jt = 0;  // running index of the piece's first tile
 
     for (int k = 0; ok && k < npc; ++k) {
-      const PieceCtx c = piece_ctx(a, load_piece(a, smem, k), kTwo);
+      const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
       const bool last_piece = k == npc - 1;
       // causal limit and sliding-window start of this row (rows past the
       // unit compute on whatever Q holds and are never stored)
@@ -476,7 +522,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       // one tile ahead so that the dependent load is off the critical path
       auto table_entry = [&](int jj) -> int {
         const int t = 2 * jj + hf;
-        return piece_entry(c, t);
+        return piece_entry<kSinks>(a, c, t);
       };
       const int j_first = (jt & 1) == grp ? 0 : 1;
       int pg_next = j_first < c.n_pt ? table_entry(j_first) : 0;
@@ -501,17 +547,18 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
         if (lane == 0) arrive_lead_relaxed(L::B_S_EMPTY + buf);  // the slice was read (wait::ld above)
 
         const int t = 2 * j + hf;  // 64-key tile of this half
-        bool page_ok = t < c.n_tiles;
+        bool page_ok = kSinks || t < c.n_tiles;  // (sinks: the masks below cover a page that no row sees)
         if (page_ok && (pg_cur < 0 || (int64_t)pg_cur >= a.num_pages)) {
           page_ok = false;
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
-        const int kb = c.key0 + kPairTileKeys * j + 64 * hf;
+        const int kb = (kSinks ? kPairTileKeys * piece_tile(p, c, j) : c.key0 + kPairTileKeys * j) + 64 * hf;
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
-        if (!(page_ok && kb >= lower && kb + 63 <= limit)) {
+        if (!(page_ok && (kb >= lower || (kSinks && kb + 63 < p.sinks)) && kb + 63 <= limit)) {
 #pragma unroll
           for (int i = 0; i < 64; ++i)
-            if (!(page_ok && kb + i >= lower && kb + i <= limit)) sv[i] = __float_as_uint(-INFINITY);
+            if (!(page_ok && (kb + i >= lower || (kSinks && kb + i < p.sinks)) && kb + i <= limit))
+              sv[i] = __float_as_uint(-INFINITY);
         }
         float mt;
         {
@@ -641,6 +688,20 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
             tmem_st32(tmem + tl + kOCol + 32u * (cc + 1), o1);
           }
           tmem_wait_st();
+        }
+        if constexpr (kSinks) {
+          if (!tile_all_seen(p, c, j)) {
+            const int sv_slot = jg % NV;
+            if (!(ok = warp_wait_cta(bar(L::B_V_LAND + sv_slot), (jg / NV) & 1, abort_flag, a.status))) break;
+            const int i = threadIdx.x & 127;  // one key of the pair tile per thread of the group
+            const int key = kPairTileKeys * piece_tile(p, c, j) + i;
+            if (key >= c.key1 || (key < c.klo && key >= p.sinks)) {
+              uint8_t* vrow = smem + L::kVOff + sv_slot * L::kVSlot + i * 128;  // [half][page][64 keys][128 B]
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                *reinterpret_cast<uint4*>(vrow + (u >> 3) * 16384 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -864,6 +925,7 @@ __device__ __forceinline__ void pair_setup(const PairParams& prm, uint8_t* smem)
     for (int i = 0; i < NV; ++i) {
       mbar_init(bar(L::B_V_FULL + i), 1);
       mbar_init(bar(L::B_V_EMPTY + i), 1);
+      mbar_init(bar(L::B_V_LAND + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::B_S_FULL + i), 1);
@@ -914,6 +976,7 @@ __device__ __forceinline__ void pair_idle_teardown(uint8_t* smem) {
   }
 }
 
+template <bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fp8_pair_kernel(const __grid_constant__ PairParams prm) {
   extern __shared__ uint8_t smem_raw[];
@@ -927,7 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The combine grid may now start (the unit counters and the table's ready
   // flag it waits on are cleared) and take the SMs of pairs that finish early.
   launch_dependents();
-  build_schedule<kPairTileKeys>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
+  build_schedule<kPairTileKeys, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
   __syncthreads();
   const int npc = info->npc;
   if (npc == 0) {  // no work for this pair (the same in both CTAs)
@@ -941,10 +1004,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        kThreads - 32 * kSoftmaxWarp0);
   // Short entries send P as two E4M3 terms; a pair with any such piece takes
   // the layout with room for both planes (the choice is the same in both CTAs).
-  if (info->two)
-    pair_cta<true>(prm, smem, npc, info->tiles);
+  // With sinks every piece has two terms.
+  if (kSinks || info->two)
+    pair_cta<true, kSinks>(prm, smem, npc, info->tiles);
   else
-    pair_cta<false>(prm, smem, npc, info->tiles);
+    pair_cta<false, false>(prm, smem, npc, info->tiles);
 }
 
 }  // namespace
@@ -962,8 +1026,10 @@ cudaError_t launch_tc_fp8_pair_partial(const DecodeArgs& a, cudaStream_t stream)
       !encode_rows_576(&prm.tm_kv_main, a.kv_cache, 1, kv_rows, 128, kTileKeys, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_rows_576(&prm.tm_kv_rope, a.kv_cache, 1, kv_rows, 64, kTileKeys, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> smem_set{0};
-  if (cudaError_t e = set_max_dynamic_smem((const void*)tc_fp8_pair_kernel, (int)kPairSmemBytes, smem_set);
+  static std::atomic<uint64_t> smem_set[2];
+  const bool sinks = plan_has_sinks(p);
+  auto* const kernel = sinks ? tc_fp8_pair_kernel<true> : tc_fp8_pair_kernel<false>;
+  if (cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)kPairSmemBytes, smem_set[sinks]);
       e != cudaSuccess)
     return e;
   // a programmatic dependent of the previous kernel in the stream (the
@@ -978,7 +1044,7 @@ cudaError_t launch_tc_fp8_pair_partial(const DecodeArgs& a, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tc_fp8_pair_kernel, prm);
+  return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
 }  // namespace mla
