@@ -481,7 +481,8 @@ extern "C" int mla_key_weights(const mla_plan* plan, const void* q, int64_t tota
   k.w_out = weights_out;
   k.out_stride = out_stride;
   k.cols = cols;
-  const cudaError_t e = launch_key_weights_simt(k, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = p.kernel == MLA_KERNEL_SIMT ? launch_key_weights_simt(k, st) : launch_key_weights_tc(k, st);
   return e == cudaSuccess ? MLA_OK : cuda_failure(e);
 }
 

@@ -160,6 +160,7 @@ cudaError_t launch_kv_pack(const void* latent, const void* rope, int64_t n, cons
 cudaError_t launch_kv_amax(const void* latent, const void* rope, int64_t n, int in_dtype, float* amax,
                            cudaStream_t stream);
 cudaError_t launch_key_weights_simt(const KeyWeightArgs& k, cudaStream_t stream);
+cudaError_t launch_key_weights_tc(const KeyWeightArgs& k, cudaStream_t stream);
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t stream);
 cudaError_t launch_combine_balanced(const DecodeArgs& a, cudaStream_t stream);
 // Zeroes `bytes` (a multiple of 16) at the 16-byte aligned `ws`, as a

@@ -1,0 +1,627 @@
+// Accumulated attention weights on the sm_100a tensor cores (mla_key_weights).
+//
+// Key j of entry b receives sum_r p_rj over the entry's query rows r that see
+// it, p_rj = exp(scale q_r . k_j - lse_r): the attention's probabilities
+// rebuilt from its log-sum-exp, so that one pass over K is enough and there
+// is no running maximum. K is read once (576 dims a key), 2 * 576 operations
+// per (row, key): a decode step (up to 128 rows an entry) is bound by HBM, a
+// step of many query tokens by the tensor cores.
+//
+// S is computed transposed, S^T = K Q^T: keys are the M dimension, so a key is
+// a TMEM lane and its sum over rows runs along the lane's columns inside one
+// thread, in a fixed order and without any exchange. CTA pairs
+// (tcgen05.mma.cta_group::2, M = 256, N <= 256): CTA c holds 128 keys (two
+// pages) of a 256-key tile and half of the N query rows, and receives its 128
+// keys' scores for all N rows.
+//
+// Both operands are cut into 128-byte column chunks (nine for 16-bit, five
+// for FP8, the last one 64 bytes wide). One operand stays in shared memory,
+// the other streams through a ring, chunk by chunk:
+//   * rows of an entry fit one group of N <= 256 (kGroups = false): Q stays,
+//     the key tiles stream. A pair takes a contiguous run of the entries'
+//     tiles, so Q is loaded once per entry it meets.
+//   * more rows (kGroups = true): a key tile stays, the row groups stream, and
+//     the sum goes on in registers from group to group; K then still comes
+//     from HBM once, and each 16 KB chunk from L2 feeds 256 x 256 x 64 (FP8:
+//     128) products. Pairs take tiles a grid apart, whose numbers of groups
+//     (causal mask, window) are alike.
+// The resident operand is replaced chunk by chunk behind the last MMAs that
+// read it.
+//
+// Roles (384 threads per CTA): warp 0 loads, warp 1 of the leader issues the
+// MMAs, warps 2 and 3 write the keys that no row sees (their old weight,
+// decayed), warps 4-11 are two groups that take alternate score buffers: ex2
+// of the score minus the row's log-sum-exp (one FMA), summed over the rows.
+// Every wait is bounded as in the attention kernels. No TMA load uses
+// multicast.
+#include <cuda.h>
+
+#include "device_common.cuh"
+#include "pair_schedule.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_common.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 256;       // keys per pair tile
+constexpr int kHalf = 128;       // keys of a tile per CTA
+constexpr int kThreads = 384;
+constexpr int kMaxEntries = 2048;  // entries of one launch: their tile counts are kept in shared memory
+constexpr int kMaxStages = 10;
+constexpr int kMaxChunks = 9;
+constexpr uint32_t kChunkBytes = 128 * 128;
+
+// shared memory, from a 1024-aligned base
+constexpr uint32_t kStartOff = 0;                                   // int [kMaxEntries + 1]: first tile of an entry
+constexpr uint32_t kLseOff = kStartOff + 8448;                      // float [group][2][256]: -lse * log2(e)
+constexpr uint32_t kLastOff = kLseOff + 4096;                       // int [group][2][256]: newest key of the row
+constexpr uint32_t kSumOff = kLastOff + 4096;                       // float [128]: group 1's sums
+constexpr uint32_t kScanOff = kSumOff + 512;                        // int [12]
+constexpr uint32_t kMiscOff = kScanOff + 64;                        // TMEM address, abort flag, loads issued
+constexpr uint32_t kBarOff = kMiscOff + 64;
+constexpr int B_FULL = 0;                          // leader, + stage: both CTAs' chunk landed
+constexpr int B_EMPTY = B_FULL + kMaxStages;       // both, + stage
+constexpr int B_RES_FULL = B_EMPTY + kMaxStages;   // leader, + chunk
+constexpr int B_RES_EMPTY = B_RES_FULL + kMaxChunks;  // both, + chunk
+constexpr int B_S_FULL = B_RES_EMPTY + kMaxChunks;    // both, + buffer
+constexpr int B_S_EMPTY = B_S_FULL + 2;            // leader, + buffer
+constexpr int B_LSE = B_S_EMPTY + 2;               // local, + group: the rows' constants are staged
+constexpr int B_SUM = B_LSE + 2;                   // local: group 1's sums are in shared memory
+constexpr int B_SUM_READ = B_SUM + 1;              // local: group 0 has read them
+constexpr int kNumBars = B_SUM_READ + 1;
+constexpr uint32_t kDataOff = 18432;
+static_assert(kBarOff + 8 * kNumBars <= kDataOff && kDataOff % 1024 == 0, "layout");
+constexpr uint32_t kSmemMax = 232448 - 1024;  // less the slack for the base's alignment
+
+struct KeyWeightParams {
+  CUtensorMap tm_q, tm_q_rope, tm_k, tm_k_rope;  // the rope maps: FP8's last 64 dims
+  KeyWeightArgs k;
+  int b0, nb;        // this launch's entries
+  int n_cols;        // N: rows per group (a multiple of 32)
+  int stages;
+  uint32_t idesc;
+};
+
+// One batch entry: keys, new tokens and their place in q, the rows' union of
+// visible keys.
+struct Entry {
+  int b, n, qlen, rows, klo;
+  int64_t q0;
+};
+__device__ __forceinline__ Entry load_entry(const KeyWeightParams& prm, int i, bool flag) {
+  const DecodeArgs& a = prm.k.a;
+  Entry e;
+  e.b = prm.b0 + i;
+  e.n = effective_seq_len(a, e.b, flag);
+  const EntryQ q = entry_q(a, e.b, flag);
+  e.q0 = q.q0;
+  e.qlen = q.qlen;
+  e.rows = q.qlen * a.plan.num_heads;
+  e.klo = a.plan.window > 0 ? max(0, e.n - e.qlen + 1 - a.plan.window) : 0;
+  return e;
+}
+// Tiles that hold a key some row sees.
+__device__ __forceinline__ int entry_tiles(const mla_plan& p, const Entry& e) {
+  if (e.n == 0 || e.qlen == 0 || e.klo >= e.n) return 0;
+  UnitGeom ug;
+  ug.klo = e.klo;
+  ug.kend = e.n;
+  return unit_tiles<kTile, true>(p, ug);
+}
+__device__ __forceinline__ int sinks_of(const mla_plan& p) { return plan_has_sinks(p) ? p.sinks : 0; }
+
+// The tiles of this pair, in the order every role walks them.
+struct Walk {
+  const int* start;  // [nb + 1]
+  int idx, end, step, i;
+  Entry e;
+  __device__ __forceinline__ Walk(const KeyWeightParams& prm, const uint8_t* smem, bool groups) {
+    start = reinterpret_cast<const int*>(smem + kStartOff);
+    const int64_t total = start[prm.nb];
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    idx = groups ? pair : (int)(total * pair / pairs);
+    end = groups ? (int)total : (int)(total * (pair + 1) / pairs);
+    step = groups ? pairs : 1;
+    i = -1;
+  }
+  __device__ __forceinline__ bool more() const { return idx < end; }
+  // moves to the entry of idx; true if it is another one than before
+  __device__ __forceinline__ bool seek(const KeyWeightParams& prm) {
+    if (i >= 0 && idx < start[i + 1]) return false;
+    do ++i;
+    while (idx >= start[i + 1]);
+    e = load_entry(prm, i, false);
+    return true;
+  }
+  __device__ __forceinline__ int tile(const mla_plan& p) const { return sink_tile<kTile>(p, e.klo, idx - start[i]); }
+  // whether this is the last tile of its entry in this pair's run
+  __device__ __forceinline__ bool last_of_entry() const { return idx + 1 >= end || idx + 1 >= start[i + 1]; }
+};
+
+// Row groups of the entry that see a key of the tile at key0.
+__device__ __forceinline__ void tile_groups(const KeyWeightParams& prm, const Entry& e, int key0, int& g0, int& g1) {
+  const mla_plan& p = prm.k.a.plan;
+  const int H = p.num_heads, N = prm.n_cols, nq = e.n - e.qlen;
+  const int t0 = min(max(key0 - nq, 0), e.qlen - 1);  // first token that sees key0
+  int64_t t1 = e.qlen;                                // past the last token whose window reaches the tile
+  if (p.window > 0 && key0 >= sinks_of(p)) t1 = min(t1, (int64_t)key0 + kTile + p.window - 1 - nq);
+  g0 = t0 * H / N;
+  g1 = ((int)t1 * H + N - 1) / N;
+}
+
+template <int E, bool kGroups>
+struct Roles {
+  static constexpr int kChunks = E == 2 ? 9 : 5;
+  static constexpr int kDims = 128 / E;  // dims of a full chunk
+  // bytes of chunk c for `rows` rows
+  static __device__ __forceinline__ uint32_t chunk_bytes(int c, int rows) {
+    return (uint32_t)rows * ((E == 1 && c == 4) ? 64u : 128u);
+  }
+};
+
+template <int E, bool kGroups>
+__device__ __forceinline__ void load_keys(const KeyWeightParams& prm, uint32_t dst, int c, int pg0, int pg1,
+                                          uint32_t full, uint64_t pol) {
+  using R = Roles<E, kGroups>;
+  const bool rope = E == 1 && c == 4;
+  const CUtensorMap* tm = rope ? &prm.tm_k_rope : &prm.tm_k;
+  tma_load_2d_pair(dst, tm, R::kDims * c, pg0 * kTileKeys, full, pol);
+  tma_load_2d_pair(dst + (rope ? 4096 : 8192), tm, R::kDims * c, pg1 * kTileKeys, full, pol);
+}
+template <int E, bool kGroups>
+__device__ __forceinline__ void load_rows(const KeyWeightParams& prm, uint32_t dst, int c, int row, uint32_t full,
+                                          uint64_t pol) {
+  using R = Roles<E, kGroups>;
+  tma_load_2d_pair(dst, (E == 1 && c == 4) ? &prm.tm_q_rope : &prm.tm_q, R::kDims * c, row, full, pol);
+}
+
+// The page of this CTA's 64 keys at `key`: its table entry where some row sees
+// them (an invalid one reads page 0; the sums leave its keys out), else page 0.
+__device__ __forceinline__ int key_page(const DecodeArgs& a, const Entry& e, int key) {
+  if (!page_seen(key, e.klo, e.n, sinks_of(a.plan))) return 0;
+  const int pg = ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + key / kTileKeys);
+  return (pg < 0 || (int64_t)pg >= a.num_pages) ? 0 : pg;
+}
+
+template <int E, bool kGroups>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tc_key_weights_kernel(const __grid_constant__ KeyWeightParams prm) {
+  using R = Roles<E, kGroups>;
+  constexpr int kChunks = R::kChunks;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const DecodeArgs& a = prm.k.a;
+  const mla_plan& p = a.plan;
+  auto bar = [&](int i) -> uint32_t { return sb + kBarOff + 8u * (uint32_t)i; };
+  auto lead = [&](int i) -> uint32_t { return mapa(bar(i), 0); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
+  int* issued = reinterpret_cast<int*>(smem + kMiscOff + 8);  // [ring chunks, resident rounds]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0 = leader
+  const int N = prm.n_cols, NB = N / 2, NS = prm.stages;
+  const int res_rows = kGroups ? kHalf : NB, ring_rows = kGroups ? NB : kHalf;
+  const uint32_t res0 = sb + kDataOff;
+  const uint32_t res_slot = (uint32_t)res_rows * 128u;  // bytes of a resident chunk's place
+  const uint32_t ring0 = (res0 + kChunks * res_slot + 1023u) & ~1023u;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i >= B_S_EMPTY && i < B_S_EMPTY + 2) count = 8;      // a group's warps in both CTAs
+      if (i >= B_LSE) count = 4;                               // a group's warps
+      mbar_init(bar(i), (uint32_t)count);
+    }
+    *abort_flag = 0;
+    issued[0] = issued[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&prm.tm_q);
+    prefetch_tmap(&prm.tm_k);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  // a programmatic dependent of the kernel before it in the stream: nothing
+  // above touches global memory
+  grid_dep_wait();
+
+  // first tile of every entry: thread runs, a scan over the block
+  {
+    int* start = reinterpret_cast<int*>(smem + kStartOff);
+    int* scan = reinterpret_cast<int*>(smem + kScanOff);
+    const int per = (prm.nb + kThreads - 1) / kThreads;
+    const int i0 = min(prm.nb, (int)threadIdx.x * per), i1 = min(prm.nb, i0 + per);
+    int run = 0;
+    for (int i = i0; i < i1; ++i) {
+      start[i] = run;
+      run += entry_tiles(p, load_entry(prm, i, blockIdx.x == 0));
+    }
+    const int incl = warp_incl_scan(run);
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int base = incl - run, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int x = scan[w];
+      if (w < warp) base += x;
+      total += x;
+    }
+    for (int i = i0; i < i1; ++i) start[i] += base;
+    if (threadIdx.x == 0) start[prm.nb] = total;
+    __syncthreads();
+  }
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_last();
+      int chunk = 0, round = 0;
+      bool ok = true;
+      Walk w(prm, smem, kGroups);
+      // one inner step: the resident operand's chunks too where `fresh`
+      auto step = [&](bool fresh, int row, int pg0, int pg1) {
+        for (int c = 0; ok && c < kChunks; ++c) {
+          const uint32_t rd = res0 + c * res_slot;
+          if (fresh) {
+            if (!(ok = bounded_wait_cta(bar(B_RES_EMPTY + c), (round & 1) ^ 1, abort_flag, a.status))) break;
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_RES_FULL + c), 2u * R::chunk_bytes(c, res_rows));
+            if (kGroups)
+              load_keys<E, kGroups>(prm, rd, c, pg0, pg1, lead(B_RES_FULL + c), pol_once);
+            else
+              load_rows<E, kGroups>(prm, rd, c, row, lead(B_RES_FULL + c), pol_again);
+          }
+          const int st = chunk % NS;
+          if (!(ok = bounded_wait_cta(bar(B_EMPTY + st), ((chunk / NS) & 1) ^ 1, abort_flag, a.status))) break;
+          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2u * R::chunk_bytes(c, ring_rows));
+          const uint32_t sd = ring0 + st * kChunkBytes;
+          if (kGroups)
+            load_rows<E, kGroups>(prm, sd, c, row, lead(B_FULL + st), pol_again);
+          else
+            load_keys<E, kGroups>(prm, sd, c, pg0, pg1, lead(B_FULL + st), pol_once);
+          ++chunk;
+        }
+        if (fresh) ++round;
+      };
+      for (; ok && w.more(); w.idx += w.step) {
+        const bool other = w.seek(prm);
+        const int key0 = kTile * w.tile(p) + kHalf * (int)rank;
+        const int pg0 = key_page(a, w.e, key0), pg1 = key_page(a, w.e, key0 + kTileKeys);
+        const int row0 = (int)(w.e.q0 * p.num_heads) + NB * (int)rank;
+        if (kGroups) {
+          int g0, g1;
+          tile_groups(prm, w.e, kTile * w.tile(p), g0, g1);
+          for (int g = g0; ok && g < g1; ++g) step(g == g0, row0 + g * N, pg0, pg1);
+        } else {
+          step(other, row0, pg0, pg1);
+        }
+      }
+      issued[0] = chunk;
+      issued[1] = round;
+      // the leader's barriers count both CTAs' bytes: nothing is in flight
+      // when the pair leaves, after an abort either
+      if (rank == 0) {
+        drain_loads(bar(B_FULL), NS, chunk);
+        if (round > 0)
+          for (int c = 0; c < kChunks; ++c) drain_phase(bar(B_RES_FULL + c), (uint32_t)(round - 1) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (leader)
+    if (rank == 0) {
+      int chunk = 0, round = 0, jt = 0;
+      bool ok = true;
+      Walk w(prm, smem, kGroups);
+      auto step = [&](bool fresh, bool last) {
+        const int buf = jt & 1;
+        if (!(ok = warp_wait(bar(B_S_EMPTY + buf), ((jt >> 1) & 1) ^ 1, abort_flag, a.status))) return;
+        const uint32_t d = tmem + 256u * buf;
+        for (int c = 0; c < kChunks; ++c) {
+          if (fresh && !(ok = warp_wait(bar(B_RES_FULL + c), round & 1, abort_flag, a.status))) return;
+          const int st = chunk % NS;
+          if (!(ok = warp_wait(bar(B_FULL + st), (chunk / NS) & 1, abort_flag, a.status))) return;
+          tc_fence_after();
+          const uint32_t rd = res0 + c * res_slot, sd = ring0 + st * kChunkBytes;
+          const bool rope = E == 1 && c == 4;
+          const uint32_t sbo = rope ? 512 : 1024, sw = rope ? kSw64 : kSw128;
+          const uint64_t dk = smem_desc(kGroups ? rd : sd, 16, sbo, sw);
+          const uint64_t dq = smem_desc(kGroups ? sd : rd, 16, sbo, sw);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the dims per MMA
+            if (rope && kk >= 2) break;
+            if constexpr (E == 2)
+              mma_f16_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+            else
+              mma_f8_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+          }
+          mma_commit_pair_mc_e(bar(B_EMPTY + st), 3);
+          if (last) mma_commit_pair_mc_e(bar(B_RES_EMPTY + c), 3);
+          ++chunk;
+        }
+        mma_commit_pair_mc_e(bar(B_S_FULL + buf), 3);
+        if (fresh) ++round;
+        ++jt;
+      };
+      for (; ok && w.more(); w.idx += w.step) {
+        const bool other = w.seek(prm);
+        if (kGroups) {
+          int g0, g1;
+          tile_groups(prm, w.e, kTile * w.tile(p), g0, g1);
+          for (int g = g0; ok && g < g1; ++g) step(g == g0, g == g1 - 1);
+        } else {
+          step(other, w.last_of_entry());
+        }
+      }
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ keys that no row sees
+    // (between sinks and window, and all keys of an entry without new tokens):
+    // the old weight, decayed
+    if ((p.window > 0 || p.varlen) && !(prm.k.w_in == prm.k.w_out && prm.k.decay == 1.f)) {
+      const int w_all = 2 * (int)gridDim.x, w_id = 2 * (int)blockIdx.x + (warp - 2);
+      const int parts = max(1, w_all / prm.nb);
+      for (int i = w_id / parts; i < prm.nb; i += w_all / parts) {
+        if (w_id / parts >= w_all / parts) break;
+        const Entry e = load_entry(prm, i, false);
+        const int n = (int)min((int64_t)e.n, prm.k.cols);
+        int k0 = 0, k1 = n;
+        if (entry_tiles(p, e) > 0) {
+          const int nst = (min(sinks_of(p), e.klo) + kTile - 1) / kTile;
+          k0 = min(n, nst * kTile);
+          k1 = min(n, e.klo / kTile * kTile);
+        }
+        const float* in = prm.k.w_in ? prm.k.w_in + (int64_t)e.b * prm.k.in_stride : nullptr;
+        float* out = prm.k.w_out + (int64_t)e.b * prm.k.out_stride;
+        for (int64_t j = k0 + 32 * (w_id % parts) + lane; j < k1; j += 32 * parts)
+          out[j] = in ? prm.k.decay * in[j] : 0.f;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ sums
+    const int grp = (warp - 4) >> 2, q = warp & 3;
+    const int tid = threadIdx.x & 127;
+    const int kl = 32 * q + lane;  // this thread's key among the CTA's 128 (its TMEM lane)
+    const uint32_t tl = (uint32_t)(32 * q) << 16;
+    float* lse_st = reinterpret_cast<float*>(smem + kLseOff) + grp * 512;  // [2][256]
+    int* last_st = reinterpret_cast<int*>(smem + kLastOff) + grp * 512;
+    float* sums = reinterpret_cast<float*>(smem + kSumOff);
+    const float sl2 = a.score_scale_log2;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    const int H = p.num_heads, sinks = sinks_of(p);
+    const int W = p.window > 0 ? p.window : 1 << 30;
+    int jt = 0, staged = 0, outer = 0;
+    bool ok = true;
+    Walk w(prm, smem, kGroups);
+
+    // the constants of rows [r0, r0 + nr) of the entry: -lse * log2(e), and the
+    // newest key each row sees (-1 past the group)
+    auto stage = [&](const Entry& e, int r0, int nr) {
+      const int at = (staged & 1) * 256;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = tid + 128 * u;
+        float x = -INFINITY;
+        int last = -1;
+        if (r < nr) {
+          const float l = prm.k.lse[e.q0 * H + r0 + r];
+          x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys adds 0
+          last = e.n - e.qlen + (r0 + r) / H;
+        }
+        lse_st[at + r] = x;
+        last_st[at + r] = last;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_LSE + grp));
+      ok = warp_wait_cta(bar(B_LSE + grp), staged & 1, abort_flag, a.status);
+      ++staged;
+    };
+    // sum over the group's rows of the scores in buffer jt & 1
+    auto sum_rows = [&](const Entry& e, int r0, int nr, int key0, bool page_ok) -> float {
+      const int at = ((staged - 1) & 1) * 256;
+      const int buf = jt & 1, key = key0 + kl;
+      if (!(ok = warp_wait_cta(bar(B_S_FULL + buf), (jt >> 1) & 1, abort_flag, a.status))) return 0.f;
+      tc_fence_after();
+      // every row of the group sees every key of this CTA's half tile
+      const int last_a = e.n - e.qlen + r0 / H, last_b = e.n - e.qlen + (r0 + nr - 1) / H;
+      const bool open = key0 + kHalf - 1 <= last_a && (key0 > last_b - W || key0 + kHalf <= sinks);
+      uint64_t s2[2] = {0ull, 0ull};
+      float s1 = 0.f;
+      for (int cb = 0; 32 * cb < nr; ++cb) {
+        uint32_t sv[32];
+        tmem_ld32(tmem + tl + 256u * buf + 32u * cb, sv);
+        tmem_wait_ld();
+        const float* lr = lse_st + at + 32 * cb;
+        if (open && 32 * cb + 32 <= nr) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(lr + i);
+            float x0, x1, x2, x3;
+            f2_unpack(fma_f32x2(f2_pack(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), sl2x2, f2_pack(l.x, l.y)),
+                      x0, x1);
+            f2_unpack(
+                fma_f32x2(f2_pack(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), sl2x2, f2_pack(l.z, l.w)),
+                x2, x3);
+            s2[0] = add_f32x2(s2[0], f2_pack(ex2_approx(x0), ex2_approx(x1)));
+            s2[1] = add_f32x2(s2[1], f2_pack(ex2_approx(x2), ex2_approx(x3)));
+          }
+        } else {
+          const int* la = last_st + at + 32 * cb;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int last = la[i];
+            const bool sees = key <= last && (key > last - W || key < sinks);
+            const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), sl2, lr[i]));
+            s1 += sees ? x : 0.f;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(bar(B_S_EMPTY + buf)); else mbar_arrive_remote_relaxed(lead(B_S_EMPTY + buf));
+      }
+      float y0, y1, y2, y3;
+      f2_unpack(s2[0], y0, y1);
+      f2_unpack(s2[1], y2, y3);
+      return page_ok ? ((y0 + y1) + (y2 + y3)) + s1 : 0.f;
+    };
+    auto old_weight = [&](const Entry& e, int key) -> float {
+      return prm.k.w_in && key < e.n && key < prm.k.cols ? prm.k.decay * prm.k.w_in[(int64_t)e.b * prm.k.in_stride + key]
+                                                         : 0.f;
+    };
+    auto page_valid = [&](const Entry& e, int key0) -> bool {
+      const int pk = key0 + (kl & ~(kTileKeys - 1));
+      if (!page_seen(pk, e.klo, e.n, sinks)) return true;
+      const int pg = ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + pk / kTileKeys);
+      if (pg >= 0 && (int64_t)pg < a.num_pages) return true;
+      if ((kl & (kTileKeys - 1)) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
+      return false;
+    };
+
+    for (; ok && w.more(); w.idx += w.step) {
+      const bool other = w.seek(prm);
+      const Entry& e = w.e;
+      const int key0 = kTile * w.tile(p) + kHalf * (int)rank, key = key0 + kl;
+      if (kGroups) {
+        int g0, g1;
+        tile_groups(prm, e, kTile * w.tile(p), g0, g1);
+        const bool page_ok = page_valid(e, key0);
+        const float old = grp == 0 ? old_weight(e, key) : 0.f;
+        float sum = 0.f;
+        for (int g = g0; ok && g < g1; ++g, ++jt) {
+          if ((jt & 1) != grp) continue;
+          const int nr = min(N, e.rows - g * N);
+          stage(e, g * N, nr);
+          if (ok) sum += sum_rows(e, g * N, nr, key0, page_ok);
+        }
+        if (!ok) break;
+        // group 1's part through shared memory, then the sum in a fixed order
+        if (grp == 1) {
+          if (outer > 0 && !(ok = warp_wait_cta(bar(B_SUM_READ), (outer - 1) & 1, abort_flag, a.status))) break;
+          sums[kl] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_SUM));
+        } else {
+          if (!(ok = warp_wait_cta(bar(B_SUM), outer & 1, abort_flag, a.status))) break;
+          sum += sums[kl];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_SUM_READ));
+          if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = old + sum;
+        }
+        ++outer;
+      } else {
+        if (other) stage(e, 0, e.rows);
+        if (!ok) break;
+        if ((jt & 1) == grp) {
+          const bool page_ok = page_valid(e, key0);
+          const float old = old_weight(e, key);
+          const float sum = sum_rows(e, 0, e.rows, key0, page_ok);
+          if (!ok) break;
+          if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = old + sum;
+        }
+        ++jt;
+      }
+    }
+    tc_fence_before();
+  }
+
+  // ---------------------------------------------------------------- teardown
+  // The leader's commits arrive in both CTAs; each waits for the last phase of
+  // every barrier they arrive on before it may leave (S_FULL was waited for).
+  __syncthreads();
+  if (warp == 2 && !*abort_flag) {
+    const int t = issued[0] - 1 - lane;
+    if (lane < NS && t >= 0) drain_phase(bar(B_EMPTY + t % NS), (uint32_t)(t / NS) & 1);
+    const int c = lane - kMaxStages;
+    if (c >= 0 && c < kChunks && issued[1] > 0) drain_phase(bar(B_RES_EMPTY + c), (uint32_t)(issued[1] - 1) & 1);
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    if (*abort_flag) spin_ns(1000000ull);  // let any MMA still in flight finish
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int E, bool kGroups>
+cudaError_t launch(const KeyWeightParams& prm, uint32_t smem, cudaStream_t stream) {
+  auto* const kernel = tc_key_weights_kernel<E, kGroups>;
+  static std::atomic<uint64_t> smem_set{0};
+  if (cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)(kSmemMax + 1024), smem_set); e != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)kNumSMs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights_tc(const KeyWeightArgs& k, cudaStream_t stream) {
+  const mla_plan& p = k.a.plan;
+  const int E = p.dtype == MLA_FP8_E4M3 ? 1 : 2;
+  const int64_t rows_max = (int64_t)p.q_len * p.num_heads;
+  // N: the entry's rows in as few groups of at most 256 as hold them, evenly
+  const int64_t groups = (rows_max + 255) / 256;
+  const int N = (int)(((rows_max + groups - 1) / groups + 31) / 32 * 32);
+  const uint64_t q_rows = (uint64_t)k.a.total_q * p.num_heads;
+  const uint64_t kv_rows = (uint64_t)k.a.num_pages * kTileKeys;
+  KeyWeightParams prm;
+  prm.k = k;
+  prm.n_cols = N;
+  const uint32_t fmt = p.dtype == MLA_BF16 ? 1u : 0u;  // BF16 = 1, FP16 = 0; E4M3 = 0 in its own kind
+  prm.idesc = instr_desc(fmt, fmt, 0, 256, (uint32_t)N);
+  // without a query token no tile is ever loaded; the maps still need an array
+  const void* q = q_rows > 0 ? k.a.q : k.a.kv_cache;
+  const uint64_t qr = q_rows > 0 ? q_rows : kv_rows;
+  const uint32_t dims = (uint32_t)(128 / E), box_q = (uint32_t)(N / 2);
+  if (!encode_rows_576(&prm.tm_q, q, E, qr, dims, box_q, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_rows_576(&prm.tm_k, k.a.kv_cache, E, kv_rows, dims, kTileKeys, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (E == 1) {
+    if (!encode_rows_576(&prm.tm_q_rope, q, E, qr, 64, box_q, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_rows_576(&prm.tm_k_rope, k.a.kv_cache, E, kv_rows, 64, kTileKeys, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  } else {
+    prm.tm_q_rope = prm.tm_q;
+    prm.tm_k_rope = prm.tm_k;
+  }
+  const bool many = groups > 1;
+  const uint32_t res = (E == 2 ? 9u : 5u) * (many ? (uint32_t)kHalf : box_q) * 128u;
+  const uint32_t data = kDataOff + ((res + 1023u) & ~1023u);
+  const int stages = (int)((kSmemMax - data) / kChunkBytes);
+  prm.stages = stages < kMaxStages ? stages : kMaxStages;
+  const uint32_t smem = data + (uint32_t)prm.stages * kChunkBytes + 1024u;
+  // entries per launch: their tile counts fit shared memory, and their sum an int
+  const int64_t tiles = (int64_t)p.max_seq_len / kTile + 2;
+  const int64_t fit = INT32_MAX / tiles;
+  const int per = (int)(fit < kMaxEntries ? fit : kMaxEntries);
+  for (int b0 = 0; b0 < p.batch; b0 += per) {
+    prm.b0 = b0;
+    prm.nb = p.batch - b0 < per ? p.batch - b0 : per;
+    const cudaError_t e = E == 2 ? (many ? launch<2, true>(prm, smem, stream) : launch<2, false>(prm, smem, stream))
+                                 : (many ? launch<1, true>(prm, smem, stream) : launch<1, false>(prm, smem, stream));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace mla
