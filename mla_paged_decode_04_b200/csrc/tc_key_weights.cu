@@ -15,18 +15,24 @@
 // keys' scores for all N rows.
 //
 // Both operands are cut into 128-byte column chunks (nine for 16-bit, five
-// for FP8, the last one 64 bytes wide). One operand stays in shared memory,
-// the other streams through a ring, chunk by chunk:
-//   * rows of an entry fit one group of N <= 256 (kGroups = false): Q stays,
-//     the key tiles stream. A pair takes a contiguous run of the entries'
-//     tiles, so Q is loaded once per entry it meets.
-//   * more rows (kGroups = true): a key tile stays, the row groups stream, and
-//     the sum goes on in registers from group to group; K then still comes
-//     from HBM once, and each 16 KB chunk from L2 feeds 256 x 256 x 64 (FP8:
-//     128) products. Pairs take tiles a grid apart, whose numbers of groups
-//     (causal mask, window) are alike.
-// The resident operand is replaced chunk by chunk behind the last MMAs that
-// read it.
+// for FP8, the last one 64 bytes wide) that go through a ring of slots; what
+// bounds the ring is the time from a slot's release to its next use (about
+// 3000 cycles: the MMAs' commit, the loader, TMA and L2, the peer's half), so
+// it has to hold that much MMA time. Three forms:
+//   * kRowsStay: an entry's rows fit one group of N <= 256 (16-bit: 128) and
+//     stay in shared memory, the key tiles stream. A pair takes a contiguous run
+//     of the entries' tiles, so Q is loaded once per entry that it meets.
+//   * kKeysStay (FP8, more rows): a key tile stays, the row groups stream. K
+//     comes from HBM once; a 16 KB chunk from L2 feeds 256 x 256 x 128 products.
+//   * kBothStream (16-bit, more than 128 rows): either resident part would take
+//     147 KB and leave a ring of 64 KB, 2048 cycles of MMAs. Without one the ring
+//     holds six slots of both operands' chunks, 3072 cycles; K is read again per
+//     group, from L2. (Ragged steps of 16 to 32 tokens x 64 heads over up to
+//     32,768 FP16 keys: @@OBS@@.)
+// With several row groups the sum goes on in registers from group to group,
+// and pairs take tiles a grid apart, whose numbers of groups (causal mask,
+// window) are alike. A resident operand is replaced slot by slot behind the
+// last MMAs that read it.
 //
 // Roles (384 threads per CTA): warp 0 loads, warp 1 of the leader issues the
 // MMAs, warps 2 and 3 write the keys that no row sees (their old weight,
@@ -49,9 +55,10 @@ using namespace ptx;
 constexpr int kTile = 256;       // keys per pair tile
 constexpr int kHalf = 128;       // keys of a tile per CTA
 constexpr int kThreads = 384;
+enum Form { kRowsStay = 0, kKeysStay = 1, kBothStream = 2 };
 constexpr int kMaxEntries = 2048;  // entries of one launch: their tile counts are kept in shared memory
-constexpr int kMaxStages = 10;
-constexpr int kMaxChunks = 9;
+constexpr int kMaxStages = 8;
+constexpr int kMaxSlots = 9;     // ring slots a tile is cut into
 constexpr uint32_t kChunkBytes = 128 * 128;
 
 // shared memory, from a 1024-aligned base
@@ -64,9 +71,9 @@ constexpr uint32_t kMiscOff = kScanOff + 64;                        // TMEM addr
 constexpr uint32_t kBarOff = kMiscOff + 64;
 constexpr int B_FULL = 0;                          // leader, + stage: both CTAs' chunk landed
 constexpr int B_EMPTY = B_FULL + kMaxStages;       // both, + stage
-constexpr int B_RES_FULL = B_EMPTY + kMaxStages;   // leader, + chunk
-constexpr int B_RES_EMPTY = B_RES_FULL + kMaxChunks;  // both, + chunk
-constexpr int B_S_FULL = B_RES_EMPTY + kMaxChunks;    // both, + buffer
+constexpr int B_RES_FULL = B_EMPTY + kMaxStages;   // leader, + slot
+constexpr int B_RES_EMPTY = B_RES_FULL + kMaxSlots;  // both, + slot
+constexpr int B_S_FULL = B_RES_EMPTY + kMaxSlots;  // both, + buffer
 constexpr int B_S_EMPTY = B_S_FULL + 2;            // leader, + buffer
 constexpr int B_LSE = B_S_EMPTY + 2;               // local, + group: the rows' constants are staged
 constexpr int B_SUM = B_LSE + 2;                   // local: group 1's sums are in shared memory
@@ -152,45 +159,54 @@ __device__ __forceinline__ void tile_groups(const KeyWeightParams& prm, const En
   g1 = ((int)t1 * H + N - 1) / N;
 }
 
-template <int E, bool kGroups>
-struct Roles {
+// A tile's column chunks of 128 bytes, kPer of them to a ring slot (one wait,
+// one commit). Larger slots cost the single issuing threads less per byte,
+// smaller ones keep a short ring finer.
+template <int E, int kPer, int kForm>
+struct Cut {
   static constexpr int kChunks = E == 2 ? 9 : 5;
+  static constexpr int kSlots = (kChunks + kPer - 1) / kPer;
   static constexpr int kDims = 128 / E;  // dims of a full chunk
-  // bytes of chunk c for `rows` rows
-  static __device__ __forceinline__ uint32_t chunk_bytes(int c, int rows) {
-    return (uint32_t)rows * ((E == 1 && c == 4) ? 64u : 128u);
+  static constexpr uint32_t kRowsAt = kForm == kBothStream ? kPer * kChunkBytes : 0;  // Q's chunks in a ring slot
+  static constexpr uint32_t kSlotBytes = kRowsAt + kPer * kChunkBytes;
+  static __host__ __device__ constexpr bool rope(int c) { return E == 1 && c == 4; }  // 64 bytes wide
+  static __host__ __device__ constexpr int first(int s) { return s * kPer; }
+  static __host__ __device__ constexpr int last(int s) { return (s + 1) * kPer < kChunks ? (s + 1) * kPer : kChunks; }
+  // bytes per row of slot s
+  static __host__ __device__ constexpr uint32_t row_bytes(int s) {
+    return (uint32_t)(last(s) - first(s)) * 128u - (rope(last(s) - 1) ? 64u : 0u);
   }
 };
 
-template <int E, bool kGroups>
+template <class C>
 __device__ __forceinline__ void load_keys(const KeyWeightParams& prm, uint32_t dst, int c, int pg0, int pg1,
                                           uint32_t full, uint64_t pol) {
-  using R = Roles<E, kGroups>;
-  const bool rope = E == 1 && c == 4;
-  const CUtensorMap* tm = rope ? &prm.tm_k_rope : &prm.tm_k;
-  tma_load_2d_pair(dst, tm, R::kDims * c, pg0 * kTileKeys, full, pol);
-  tma_load_2d_pair(dst + (rope ? 4096 : 8192), tm, R::kDims * c, pg1 * kTileKeys, full, pol);
+  const CUtensorMap* tm = C::rope(c) ? &prm.tm_k_rope : &prm.tm_k;
+  tma_load_2d_pair(dst, tm, C::kDims * c, pg0 * kTileKeys, full, pol);
+  tma_load_2d_pair(dst + (C::rope(c) ? 4096 : 8192), tm, C::kDims * c, pg1 * kTileKeys, full, pol);
 }
-template <int E, bool kGroups>
+template <class C>
 __device__ __forceinline__ void load_rows(const KeyWeightParams& prm, uint32_t dst, int c, int row, uint32_t full,
                                           uint64_t pol) {
-  using R = Roles<E, kGroups>;
-  tma_load_2d_pair(dst, (E == 1 && c == 4) ? &prm.tm_q_rope : &prm.tm_q, R::kDims * c, row, full, pol);
+  tma_load_2d_pair(dst, C::rope(c) ? &prm.tm_q_rope : &prm.tm_q, C::kDims * c, row, full, pol);
 }
 
-// The page of this CTA's 64 keys at `key`: its table entry where some row sees
-// them (an invalid one reads page 0; the sums leave its keys out), else page 0.
-__device__ __forceinline__ int key_page(const DecodeArgs& a, const Entry& e, int key) {
+// The table entry of the 64 keys at `key` where some row sees them, else page
+// 0. Read a tile ahead of its use.
+__device__ __forceinline__ int key_entry(const DecodeArgs& a, const Entry& e, int key) {
   if (!page_seen(key, e.klo, e.n, sinks_of(a.plan))) return 0;
-  const int pg = ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + key / kTileKeys);
-  return (pg < 0 || (int64_t)pg >= a.num_pages) ? 0 : pg;
+  return ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + key / kTileKeys);
 }
+__device__ __forceinline__ bool page_valid(const DecodeArgs& a, int pg) { return pg >= 0 && (int64_t)pg < a.num_pages; }
+// an entry outside the cache reads page 0 (the sums leave its keys out)
+__device__ __forceinline__ int page_or_0(const DecodeArgs& a, int pg) { return page_valid(a, pg) ? pg : 0; }
 
-template <int E, bool kGroups>
+template <int E, int kForm, int kPer>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_key_weights_kernel(const __grid_constant__ KeyWeightParams prm) {
-  using R = Roles<E, kGroups>;
-  constexpr int kChunks = R::kChunks;
+  using C = Cut<E, kPer, kForm>;
+  constexpr bool kGroups = kForm != kRowsStay;    // an entry may have several row groups
+  constexpr bool kStays = kForm != kBothStream;   // one operand is resident
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -200,14 +216,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto lead = [&](int i) -> uint32_t { return mapa(bar(i), 0); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
-  int* issued = reinterpret_cast<int*>(smem + kMiscOff + 8);  // [ring chunks, resident rounds]
+  int* issued = reinterpret_cast<int*>(smem + kMiscOff + 8);  // [ring slots, resident rounds]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0 = leader
   const int N = prm.n_cols, NB = N / 2, NS = prm.stages;
-  const int res_rows = kGroups ? kHalf : NB, ring_rows = kGroups ? NB : kHalf;
+  // rows of a chunk, both operands' CTA halves: what stays, what a slot takes
+  const int res_rows = kForm == kKeysStay ? kHalf : NB;
+  const int ring_rows = kForm == kRowsStay ? kHalf : kForm == kKeysStay ? NB : kHalf + NB;
   const uint32_t res0 = sb + kDataOff;
-  const uint32_t res_slot = (uint32_t)res_rows * 128u;  // bytes of a resident chunk's place
-  const uint32_t ring0 = (res0 + kChunks * res_slot + 1023u) & ~1023u;
+  const uint32_t res_slot = kStays ? (uint32_t)res_rows * 128u : 0u;  // bytes of a resident chunk's place
+  const uint32_t ring0 = (res0 + C::kChunks * res_slot + 1023u) & ~1023u;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -265,87 +283,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_last();
-      int chunk = 0, round = 0;
+      int filled = 0, round = 0, st = 0;
+      uint32_t ph = 1;  // parity to wait for: the ring starts empty
       bool ok = true;
       Walk w(prm, smem, kGroups);
-      // one inner step: the resident operand's chunks too where `fresh`
+      const uint32_t full0 = lead(B_FULL), res_full0 = lead(B_RES_FULL);
+      // one inner step: the resident operand's slots too where `fresh`
       auto step = [&](bool fresh, int row, int pg0, int pg1) {
-        for (int c = 0; ok && c < kChunks; ++c) {
-          const uint32_t rd = res0 + c * res_slot;
-          if (fresh) {
-            if (!(ok = bounded_wait_cta(bar(B_RES_EMPTY + c), (round & 1) ^ 1, abort_flag, a.status))) break;
-            if (rank == 0) mbar_arrive_expect_tx(bar(B_RES_FULL + c), 2u * R::chunk_bytes(c, res_rows));
-            if (kGroups)
-              load_keys<E, kGroups>(prm, rd, c, pg0, pg1, lead(B_RES_FULL + c), pol_once);
-            else
-              load_rows<E, kGroups>(prm, rd, c, row, lead(B_RES_FULL + c), pol_again);
+#pragma unroll
+        for (int s = 0; s < C::kSlots; ++s) {
+          if (kStays && fresh) {
+            if (!(ok = bounded_wait_cta(bar(B_RES_EMPTY + s), (round & 1) ^ 1, abort_flag, a.status))) return;
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_RES_FULL + s), 2u * (uint32_t)res_rows * C::row_bytes(s));
+#pragma unroll
+            for (int c = C::first(s); c < C::last(s); ++c) {
+              if (kForm == kKeysStay)
+                load_keys<C>(prm, res0 + c * res_slot, c, pg0, pg1, res_full0 + 8u * s, pol_once);
+              else
+                load_rows<C>(prm, res0 + c * res_slot, c, row, res_full0 + 8u * s, pol_again);
+            }
           }
-          const int st = chunk % NS;
-          if (!(ok = bounded_wait_cta(bar(B_EMPTY + st), ((chunk / NS) & 1) ^ 1, abort_flag, a.status))) break;
-          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2u * R::chunk_bytes(c, ring_rows));
-          const uint32_t sd = ring0 + st * kChunkBytes;
-          if (kGroups)
-            load_rows<E, kGroups>(prm, sd, c, row, lead(B_FULL + st), pol_again);
-          else
-            load_keys<E, kGroups>(prm, sd, c, pg0, pg1, lead(B_FULL + st), pol_once);
-          ++chunk;
+          if (!(ok = bounded_wait_cta(bar(B_EMPTY + st), ph, abort_flag, a.status))) return;
+          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2u * (uint32_t)ring_rows * C::row_bytes(s));
+          const uint32_t sd = ring0 + st * C::kSlotBytes, full = full0 + 8u * st;
+#pragma unroll
+          for (int c = C::first(s); c < C::last(s); ++c) {
+            const uint32_t cd = sd + (c - C::first(s)) * kChunkBytes;
+            if (kForm != kKeysStay)
+              load_keys<C>(prm, cd, c, pg0, pg1, full, kForm == kRowsStay ? pol_once : pol_again);
+            if (kForm != kRowsStay) load_rows<C>(prm, cd + C::kRowsAt, c, row, full, pol_again);
+          }
+          ++filled;
+          if (++st == NS) st = 0, ph ^= 1;
         }
         if (fresh) ++round;
       };
-      for (; ok && w.more(); w.idx += w.step) {
-        const bool other = w.seek(prm);
+      bool other = w.more() && w.seek(prm);
+      int e0 = 0, e1 = 0;
+      auto entries = [&]() {
         const int key0 = kTile * w.tile(p) + kHalf * (int)rank;
-        const int pg0 = key_page(a, w.e, key0), pg1 = key_page(a, w.e, key0 + kTileKeys);
+        e0 = key_entry(a, w.e, key0);
+        e1 = key_entry(a, w.e, key0 + kTileKeys);
+      };
+      if (w.more()) entries();
+      while (ok && w.more()) {
+        const int pg0 = page_or_0(a, e0), pg1 = page_or_0(a, e1);
         const int row0 = (int)(w.e.q0 * p.num_heads) + NB * (int)rank;
+        const bool fresh = other;
+        int g0 = 0, g1 = 1;
+        if (kGroups) tile_groups(prm, w.e, kTile * w.tile(p), g0, g1);
+        // the next tile's entries are on their way while this one's chunks are issued
+        w.idx += w.step;
+        if (w.more()) {
+          other = w.seek(prm);
+          entries();
+        }
         if (kGroups) {
-          int g0, g1;
-          tile_groups(prm, w.e, kTile * w.tile(p), g0, g1);
           for (int g = g0; ok && g < g1; ++g) step(g == g0, row0 + g * N, pg0, pg1);
         } else {
-          step(other, row0, pg0, pg1);
+          step(fresh, row0, pg0, pg1);
         }
       }
-      issued[0] = chunk;
+      issued[0] = filled;
       issued[1] = round;
       // the leader's barriers count both CTAs' bytes: nothing is in flight
       // when the pair leaves, after an abort either
       if (rank == 0) {
-        drain_loads(bar(B_FULL), NS, chunk);
-        if (round > 0)
-          for (int c = 0; c < kChunks; ++c) drain_phase(bar(B_RES_FULL + c), (uint32_t)(round - 1) & 1);
+        drain_loads(bar(B_FULL), NS, filled);
+        if (kStays && round > 0)
+          for (int s = 0; s < C::kSlots; ++s) drain_phase(bar(B_RES_FULL + s), (uint32_t)(round - 1) & 1);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (rank == 0) {
-      int chunk = 0, round = 0, jt = 0;
+      int round = 0, jt = 0, st = 0;
+      uint32_t ph = 0;
       bool ok = true;
       Walk w(prm, smem, kGroups);
+      // operand descriptors: chunk c is c * res_slot further in the resident
+      // part, (c % kPer) * 16 KB in a ring slot (in 16-byte units); the FP8 rope
+      // chunk has the 64-byte swizzle and half the row stride
+      const uint64_t res_desc = smem_desc(res0, 16, 1024, kSw128), ring_desc = smem_desc(ring0, 16, 1024, kSw128);
+      const uint64_t rope_bits = smem_desc(0, 16, 512, kSw64) - smem_desc(0, 16, 1024, kSw128);
       auto step = [&](bool fresh, bool last) {
         const int buf = jt & 1;
         if (!(ok = warp_wait(bar(B_S_EMPTY + buf), ((jt >> 1) & 1) ^ 1, abort_flag, a.status))) return;
         const uint32_t d = tmem + 256u * buf;
-        for (int c = 0; c < kChunks; ++c) {
-          if (fresh && !(ok = warp_wait(bar(B_RES_FULL + c), round & 1, abort_flag, a.status))) return;
-          const int st = chunk % NS;
-          if (!(ok = warp_wait(bar(B_FULL + st), (chunk / NS) & 1, abort_flag, a.status))) return;
-          tc_fence_after();
-          const uint32_t rd = res0 + c * res_slot, sd = ring0 + st * kChunkBytes;
-          const bool rope = E == 1 && c == 4;
-          const uint32_t sbo = rope ? 512 : 1024, sw = rope ? kSw64 : kSw128;
-          const uint64_t dk = smem_desc(kGroups ? rd : sd, 16, sbo, sw);
-          const uint64_t dq = smem_desc(kGroups ? sd : rd, 16, sbo, sw);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the dims per MMA
-            if (rope && kk >= 2) break;
-            if constexpr (E == 2)
-              mma_f16_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
-            else
-              mma_f8_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+        for (int s = 0; s < C::kSlots; ++s) {
+          if (kStays && fresh && !(ok = warp_wait(bar(B_RES_FULL + s), round & 1, abort_flag, a.status))) return;
+          if (!(ok = warp_wait(bar(B_FULL + st), ph, abort_flag, a.status))) return;
+          tc_fence_after();
+          const uint64_t slot_desc = ring_desc + (uint64_t)(st * (C::kSlotBytes >> 4));
+#pragma unroll
+          for (int c = C::first(s); c < C::last(s); ++c) {
+            const uint64_t more = C::rope(c) ? rope_bits : 0ull;
+            const uint64_t dr = res_desc + (uint64_t)(c * (res_slot >> 4)) + more;
+            const uint64_t ds = slot_desc + (uint64_t)((c - C::first(s)) * (kChunkBytes >> 4)) + more;
+            const uint64_t dk = kForm == kKeysStay ? dr : ds;
+            const uint64_t dq = kForm == kRowsStay ? dr : ds + (C::kRowsAt >> 4);
+#pragma unroll
+            for (int kk = 0; kk < (C::rope(c) ? 2 : 4); ++kk) {  // 32 bytes of the dims per MMA
+              if constexpr (E == 2)
+                mma_f16_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+              else
+                mma_f8_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+            }
           }
           mma_commit_pair_mc_e(bar(B_EMPTY + st), 3);
-          if (last) mma_commit_pair_mc_e(bar(B_RES_EMPTY + c), 3);
-          ++chunk;
+          if (kStays && last) mma_commit_pair_mc_e(bar(B_RES_EMPTY + s), 3);
+          if (++st == NS) st = 0, ph ^= 1;
         }
         mma_commit_pair_mc_e(bar(B_S_FULL + buf), 3);
         if (fresh) ++round;
@@ -424,11 +472,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait_cta(bar(B_LSE + grp), staged & 1, abort_flag, a.status);
       ++staged;
     };
-    // sum over the group's rows of the scores in buffer jt & 1
-    auto sum_rows = [&](const Entry& e, int r0, int nr, int key0, bool page_ok) -> float {
+    // sum over the group's rows of item t's scores (buffer t & 1)
+    auto sum_rows = [&](const Entry& e, int r0, int nr, int key0, int t) -> float {
       const int at = ((staged - 1) & 1) * 256;
-      const int buf = jt & 1, key = key0 + kl;
-      if (!(ok = warp_wait_cta(bar(B_S_FULL + buf), (jt >> 1) & 1, abort_flag, a.status))) return 0.f;
+      const int buf = t & 1, key = key0 + kl;
+      if (!(ok = warp_wait_cta(bar(B_S_FULL + buf), (t >> 1) & 1, abort_flag, a.status))) return 0.f;
       tc_fence_after();
       // every row of the group sees every key of this CTA's half tile
       const int last_a = e.n - e.qlen + r0 / H, last_b = e.n - e.qlen + (r0 + nr - 1) / H;
@@ -472,36 +520,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float y0, y1, y2, y3;
       f2_unpack(s2[0], y0, y1);
       f2_unpack(s2[1], y2, y3);
-      return page_ok ? ((y0 + y1) + (y2 + y3)) + s1 : 0.f;
+      return ((y0 + y1) + (y2 + y3)) + s1;
     };
-    auto old_weight = [&](const Entry& e, int key) -> float {
-      return prm.k.w_in && key < e.n && key < prm.k.cols ? prm.k.decay * prm.k.w_in[(int64_t)e.b * prm.k.in_stride + key]
-                                                         : 0.f;
+    // this thread's key of a tile: its old weight and its page's table entry,
+    // read one tile ahead
+    struct Ahead {
+      float old;
+      int entry;
     };
-    auto page_valid = [&](const Entry& e, int key0) -> bool {
-      const int pk = key0 + (kl & ~(kTileKeys - 1));
-      if (!page_seen(pk, e.klo, e.n, sinks)) return true;
-      const int pg = ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + pk / kTileKeys);
-      if (pg >= 0 && (int64_t)pg < a.num_pages) return true;
+    auto ahead = [&](const Entry& e, int key0) -> Ahead {
+      Ahead h;
+      const int key = key0 + kl;
+      h.old = prm.k.w_in && key < e.n && key < prm.k.cols ? prm.k.w_in[(int64_t)e.b * prm.k.in_stride + key] : 0.f;
+      h.entry = key_entry(a, e, key0 + (kl & ~(kTileKeys - 1)));
+      return h;
+    };
+    auto check_page = [&](int entry) -> bool {
+      if (page_valid(a, entry)) return true;
       if ((kl & (kTileKeys - 1)) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
       return false;
     };
+    auto write = [&](const Entry& e, int key, float old, float sum) {
+      if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = prm.k.decay * old + sum;
+    };
+    auto tile_key = [&]() -> int { return kTile * w.tile(p) + kHalf * (int)rank; };
 
-    for (; ok && w.more(); w.idx += w.step) {
-      const bool other = w.seek(prm);
-      const Entry& e = w.e;
-      const int key0 = kTile * w.tile(p) + kHalf * (int)rank, key = key0 + kl;
-      if (kGroups) {
+    if constexpr (kGroups) {
+      Ahead next{0.f, 0};
+      if (w.more()) {
+        w.seek(prm);
+        next = ahead(w.e, tile_key());
+      }
+      while (ok && w.more()) {
+        const Entry e = w.e;
+        const int key0 = tile_key(), key = key0 + kl;
+        const Ahead cur = next;
         int g0, g1;
         tile_groups(prm, e, kTile * w.tile(p), g0, g1);
-        const bool page_ok = page_valid(e, key0);
-        const float old = grp == 0 ? old_weight(e, key) : 0.f;
+        w.idx += w.step;
+        if (w.more()) {
+          w.seek(prm);
+          next = ahead(w.e, tile_key());
+        }
         float sum = 0.f;
         for (int g = g0; ok && g < g1; ++g, ++jt) {
           if ((jt & 1) != grp) continue;
           const int nr = min(N, e.rows - g * N);
           stage(e, g * N, nr);
-          if (ok) sum += sum_rows(e, g * N, nr, key0, page_ok);
+          if (ok) sum += sum_rows(e, g * N, nr, key0, jt);
         }
         if (!ok) break;
         // group 1's part through shared memory, then the sum in a fixed order
@@ -515,20 +581,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sum += sums[kl];
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_SUM_READ));
-          if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = old + sum;
+          write(e, key, cur.old, check_page(cur.entry) ? sum : 0.f);
         }
         ++outer;
-      } else {
-        if (other) stage(e, 0, e.rows);
-        if (!ok) break;
-        if ((jt & 1) == grp) {
-          const bool page_ok = page_valid(e, key0);
-          const float old = old_weight(e, key);
-          const float sum = sum_rows(e, 0, e.rows, key0, page_ok);
-          if (!ok) break;
-          if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = old + sum;
+      }
+    } else {
+      // the group's tiles are every other one of the pair's run; an entry's
+      // constants are staged by both groups when the run reaches it
+      int staged_for = -1;
+      auto to_own = [&]() {  // to the group's next tile; the entries passed on the way
+        while (ok && w.more()) {
+          w.seek(prm);
+          if ((jt & 1) == grp) return;
+          ++w.idx, ++jt;
         }
-        ++jt;
+      };
+      to_own();
+      Ahead next{0.f, 0};
+      if (w.more()) next = ahead(w.e, tile_key());
+      while (ok && w.more()) {
+        const Entry e = w.e;
+        const int key0 = tile_key(), key = key0 + kl, t = jt;
+        const Ahead cur = next;
+        if (staged_for != e.b) {
+          stage(e, 0, e.rows);
+          staged_for = e.b;
+          if (!ok) break;
+        }
+        ++w.idx, ++jt;
+        to_own();
+        if (w.more()) next = ahead(w.e, tile_key());
+        const float sum = sum_rows(e, 0, e.rows, key0, t);
+        if (!ok) break;
+        write(e, key, cur.old, check_page(cur.entry) ? sum : 0.f);
       }
     }
     tc_fence_before();
@@ -541,8 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 2 && !*abort_flag) {
     const int t = issued[0] - 1 - lane;
     if (lane < NS && t >= 0) drain_phase(bar(B_EMPTY + t % NS), (uint32_t)(t / NS) & 1);
-    const int c = lane - kMaxStages;
-    if (c >= 0 && c < kChunks && issued[1] > 0) drain_phase(bar(B_RES_EMPTY + c), (uint32_t)(issued[1] - 1) & 1);
+    const int s = lane - kMaxStages;
+    if (kStays && s >= 0 && s < C::kSlots && issued[1] > 0) drain_phase(bar(B_RES_EMPTY + s), (uint32_t)(issued[1] - 1) & 1);
   }
   __syncthreads();
   tc_fence_before();
@@ -554,9 +639,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int E, bool kGroups>
-cudaError_t launch(const KeyWeightParams& prm, uint32_t smem, cudaStream_t stream) {
-  auto* const kernel = tc_key_weights_kernel<E, kGroups>;
+template <int E, int kForm, int kPer>
+cudaError_t launch(KeyWeightParams& prm, cudaStream_t stream) {
+  using C = Cut<E, kPer, kForm>;
+  const uint32_t res = kForm == kBothStream ? 0u
+                       : C::kChunks * (kForm == kKeysStay ? (uint32_t)kHalf : (uint32_t)prm.n_cols / 2) * 128u;
+  const uint32_t data = kDataOff + ((res + 1023u) & ~1023u);
+  const int stages = (int)((kSmemMax - data) / C::kSlotBytes);
+  prm.stages = stages < kMaxStages ? stages : kMaxStages;
+  const uint32_t smem = data + (uint32_t)prm.stages * C::kSlotBytes + 1024u;
+  auto* const kernel = tc_key_weights_kernel<E, kForm, kPer>;
   static std::atomic<uint64_t> smem_set{0};
   if (cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)(kSmemMax + 1024), smem_set); e != cudaSuccess)
     return e;
@@ -604,12 +696,6 @@ cudaError_t launch_key_weights_tc(const KeyWeightArgs& k, cudaStream_t stream) {
     prm.tm_q_rope = prm.tm_q;
     prm.tm_k_rope = prm.tm_k;
   }
-  const bool many = groups > 1;
-  const uint32_t res = (E == 2 ? 9u : 5u) * (many ? (uint32_t)kHalf : box_q) * 128u;
-  const uint32_t data = kDataOff + ((res + 1023u) & ~1023u);
-  const int stages = (int)((kSmemMax - data) / kChunkBytes);
-  prm.stages = stages < kMaxStages ? stages : kMaxStages;
-  const uint32_t smem = data + (uint32_t)prm.stages * kChunkBytes + 1024u;
   // entries per launch: their tile counts fit shared memory, and their sum an int
   const int64_t tiles = (int64_t)p.max_seq_len / kTile + 2;
   const int64_t fit = INT32_MAX / tiles;
@@ -617,8 +703,11 @@ cudaError_t launch_key_weights_tc(const KeyWeightArgs& k, cudaStream_t stream) {
   for (int b0 = 0; b0 < p.batch; b0 += per) {
     prm.b0 = b0;
     prm.nb = p.batch - b0 < per ? p.batch - b0 : per;
-    const cudaError_t e = E == 2 ? (many ? launch<2, true>(prm, smem, stream) : launch<2, false>(prm, smem, stream))
-                                 : (many ? launch<1, true>(prm, smem, stream) : launch<1, false>(prm, smem, stream));
+    cudaError_t e;
+    if (E == 1)
+      e = groups > 1 ? launch<1, kKeysStay, 2>(prm, stream) : launch<1, kRowsStay, 2>(prm, stream);
+    else
+      e = N > 128 ? launch<2, kBothStream, 1>(prm, stream) : launch<2, kRowsStay, 2>(prm, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
