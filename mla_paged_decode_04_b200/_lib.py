@@ -22,6 +22,7 @@ LIB_PATH = CHECK_LIB_PATH if os.environ.get("MLA_DECODE_BOUNDS_CHECK", "0") == "
 
 MLA_BF16, MLA_FP16, MLA_FP8_E4M3 = 0, 1, 2
 DTYPES = {"bf16": MLA_BF16, "fp16": MLA_FP16, "fp8": MLA_FP8_E4M3}
+_TORCH_CODES = {torch.bfloat16: MLA_BF16, torch.float16: MLA_FP16, torch.float8_e4m3fn: MLA_FP8_E4M3}
 MLA_KERNEL_AUTO, MLA_KERNEL_TCGEN05, MLA_KERNEL_SIMT, MLA_KERNEL_TCGEN05_SOLO = 0, 1, 2, 3
 KERNELS = {"auto": MLA_KERNEL_AUTO, "tcgen05": MLA_KERNEL_TCGEN05, "simt": MLA_KERNEL_SIMT,
            "tcgen05_solo": MLA_KERNEL_TCGEN05_SOLO}
@@ -150,13 +151,8 @@ def mla_version() -> str:
 def _dtype_code(dtype) -> int:
     if isinstance(dtype, str):
         return DTYPES[dtype]
-    if dtype == torch.bfloat16:
-        return MLA_BF16
-    if dtype == torch.float16:
-        return MLA_FP16
-    if dtype == torch.float8_e4m3fn:
-        return MLA_FP8_E4M3
-    return int(dtype)
+    code = _TORCH_CODES.get(dtype)
+    return int(dtype) if code is None else code
 
 
 def mla_decode_plan(batch, q_len, num_heads, max_seq_len, dtype) -> MlaPlan:
@@ -206,18 +202,22 @@ def mla_prefill_plan(batch, max_q_len, num_heads, max_seq_len, dtype, split_kv=0
     return p
 
 
+# Small calls are bound by the host: the helpers below take the cheapest
+# accessor of each property (device indexes instead of device objects, the raw
+# stream instead of a Stream object, plain integers for pointers).
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _check_tensors(q, **named):
+def _check_tensors(q, /, **named):
     """Every tensor argument is a contiguous CUDA tensor on q's device."""
     if not (isinstance(q, torch.Tensor) and q.is_cuda):
         raise ValueError("q must be a CUDA tensor")
+    index = q.get_device()
     for k, t in named.items():
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != q.device:
+        if not isinstance(t, torch.Tensor) or t.get_device() != index:
             raise ValueError(f"{k} must be a CUDA tensor on {q.device} (got "
                              f"{t.device if isinstance(t, torch.Tensor) else type(t).__name__})")
         if not t.is_contiguous():
@@ -232,16 +232,11 @@ def _call(name, plan, q, kv_cache, block_tables, seq_lens, softmax_scale, out, l
           q_scale, kv_scale, stream):
     _check_tensors(q, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, out=out,
                    lse=lse, workspace=workspace)
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device).cuda_stream if q.is_cuda else 0
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    num_pages, page_size = int(kv_cache.shape[0]), int(kv_cache.shape[1])
-    rc = getattr(_lib, name)(ctypes.byref(plan), _ptr(q), _ptr(kv_cache), num_pages, page_size,
-                         _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens),
-                         float(softmax_scale), float(q_scale), float(kv_scale), _ptr(out),
-                         _ptr(lse), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
-                         ctypes.c_void_p(stream))
+    rc = getattr(_lib, name)(ctypes.byref(plan), _ptr(q), _ptr(kv_cache), kv_cache.size(0), kv_cache.size(1),
+                             _ptr(block_tables), block_tables.size(1), _ptr(seq_lens),
+                             float(softmax_scale), float(q_scale), float(kv_scale), _ptr(out),
+                             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _stream_of(q, stream))
     if rc != 0:
         raise MlaError(rc, name)
 
@@ -283,7 +278,7 @@ def _call_prefill(name, plan, q, cu_seqlens_q, kv_cache, block_tables, seq_lens,
                              num_pages, page_size, _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens),
                              float(softmax_scale), float(q_scale), float(kv_scale), _ptr(out), _ptr(lse),
                              _ptr(workspace), int(workspace.numel() * workspace.element_size()),
-                             ctypes.c_void_p(_stream_of(q, stream)))
+                             _stream_of(q, stream))
     if rc != 0:
         raise MlaError(rc, name)
 
@@ -316,8 +311,9 @@ def mla_decode_status(workspace, clear=True, stream=None) -> int:
 
 
 def _stream_of(t, stream):
+    """The raw cudaStream_t to launch on: torch's current stream of t's device unless `stream` is given."""
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
@@ -337,7 +333,7 @@ def kv_pack(latent, rope, slot_mapping, kv_cache, kv_scale=1.0, device_status=No
     cache_dtype = _dtype_code(kv_cache.dtype)
     rc = _lib.mla_kv_pack(_ptr(latent), _ptr(rope), int(latent.shape[0]), _ptr(slot_mapping), _ptr(kv_cache),
                           int(kv_cache.shape[0]), int(kv_cache.shape[1]), in_dtype, cache_dtype, float(kv_scale),
-                          _ptr(device_status), ctypes.c_void_p(_stream_of(latent, stream)))
+                          _ptr(device_status), _stream_of(latent, stream))
     if rc != 0:
         raise MlaError(rc, "mla_kv_pack")
 
@@ -348,19 +344,20 @@ def kv_amax(latent, rope, out=None, stream=None) -> torch.Tensor:
         out = torch.empty(1, dtype=torch.float32, device=latent.device)
     _check_tensors(latent, rope=rope, out=out)
     rc = _lib.mla_kv_amax(_ptr(latent), _ptr(rope), int(latent.shape[0]), _dtype_code(latent.dtype), _ptr(out),
-                          ctypes.c_void_p(_stream_of(latent, stream)))
+                          _stream_of(latent, stream))
     if rc != 0:
         raise MlaError(rc, "mla_kv_amax")
     return out
 
 
-def _weight_rows(name, t, device):
-    """Checks an fp32 [B, columns] tensor whose rows may lie apart; returns its row stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != torch.float32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _weight_rows(name, t, index):
+    """Checks an fp32 [B, columns] tensor on device `index` whose rows may lie apart; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not torch.float32 or t.dim() != 2 or (t.stride(1) != 1 and t.size(1) > 1):
         raise ValueError(f"{name} must be float32 [batch, columns] with adjacent columns")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+    stride = t.stride(0)
+    return stride if t.size(0) > 1 else max(stride, t.size(1))
 
 
 def key_weights(plan: MlaPlan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, device_status,
@@ -372,40 +369,39 @@ def key_weights(plan: MlaPlan, q, kv_cache, block_tables, seq_lens, softmax_scal
     `weights` and `out` are fp32 [B, columns] (rows may be strided) and may be the same tensor; weights = None counts
     as zeros. device_status: an int32 device word for MLA_DEV_* bits. See include/mla_decode.h.
     """
-    _check_tensors(q, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, lse=lse,
+    _check_tensors(q, q=q, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, lse=lse,
                    cu_seqlens_q=cu_seqlens_q, device_status=device_status)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    if q.dtype != kv_cache.dtype or _dtype_code(q.dtype) != plan.dtype:
+    index, batch = q.get_device(), plan.batch
+    dtype, rows = q.dtype, q.numel() // 576
+    if dtype is not kv_cache.dtype or _TORCH_CODES.get(dtype) != plan.dtype:
         raise ValueError("q and kv_cache must have the plan's dtype")
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != 576 or q.shape[-1] != 576:
+    if kv_cache.dim() != 3 or kv_cache.size(2) != 576 or q.size(-1) != 576:
         raise ValueError("q and kv_cache must have 576 dims")
-    rows = q.numel() // 576
-    if not plan.varlen and rows != plan.batch * plan.q_len * plan.num_heads:
+    if plan.varlen:
+        if q.dim() != 3 or q.size(1) != plan.num_heads:
+            raise ValueError("q must be [total_q, num_heads, 576]")
+        if cu_seqlens_q is not None and (cu_seqlens_q.dtype is not torch.int32 or cu_seqlens_q.numel() != batch + 1):
+            raise ValueError("cu_seqlens_q must be int32 [batch + 1]")
+    elif rows != batch * plan.q_len * plan.num_heads:
         raise ValueError("q must be [batch, q_len, num_heads, 576] of the plan")
-    if plan.varlen and (q.dim() != 3 or q.shape[1] != plan.num_heads):
-        raise ValueError("q must be [total_q, num_heads, 576]")
-    if cu_seqlens_q is not None and (cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.numel() != plan.batch + 1):
-        raise ValueError("cu_seqlens_q must be int32 [batch + 1]")
-    if lse is None or lse.dtype != torch.float32 or lse.numel() != rows:
+    if lse is None or lse.dtype is not torch.float32 or lse.numel() != rows:
         raise ValueError("lse must be float32 with one value per query row")
-    if device_status is None or device_status.dtype != torch.int32:
+    if device_status is None or device_status.dtype is not torch.int32:
         raise ValueError("device_status must be an int32 CUDA tensor")
-    if block_tables.dim() != 2 or block_tables.shape[0] != plan.batch or seq_lens.numel() != plan.batch:
+    if block_tables.dim() != 2 or block_tables.size(0) != batch or seq_lens.numel() != batch:
         raise ValueError("block_tables and seq_lens must have one row per batch entry")
-    out_stride = _weight_rows("out", out, q.device)
-    in_stride, cols = 0, int(out.shape[1])
+    out_stride, in_stride = _weight_rows("out", out, index), 0
+    if out.size(0) != batch:
+        raise ValueError("out must have one row per batch entry")
     if weights is not None:
-        in_stride = _weight_rows("weights", weights, q.device)
+        in_stride = _weight_rows("weights", weights, index)
         if weights.shape != out.shape:
             raise ValueError("weights and out must have one shape")
-    if out.shape[0] != plan.batch:
-        raise ValueError("out must have one row per batch entry")
-    rc = _lib.mla_key_weights(ctypes.byref(plan), _ptr(q), int(q.shape[0]), _ptr(cu_seqlens_q), _ptr(kv_cache),
-                              int(kv_cache.shape[0]), int(kv_cache.shape[1]), _ptr(block_tables),
-                              int(block_tables.shape[1]), _ptr(seq_lens), float(softmax_scale), float(q_scale),
-                              float(kv_scale), _ptr(lse), _ptr(weights), in_stride, float(decay), _ptr(out),
-                              out_stride, cols, _ptr(device_status), ctypes.c_void_p(_stream_of(q, stream)))
+    rc = _lib.mla_key_weights(ctypes.byref(plan), _ptr(q), q.size(0), _ptr(cu_seqlens_q), _ptr(kv_cache),
+                              kv_cache.size(0), kv_cache.size(1), _ptr(block_tables), block_tables.size(1),
+                              _ptr(seq_lens), float(softmax_scale), float(q_scale), float(kv_scale), _ptr(lse),
+                              _ptr(weights), in_stride, float(decay), _ptr(out), out_stride, out.size(1),
+                              _ptr(device_status), _stream_of(q, stream))
     if rc != 0:
         raise MlaError(rc, "mla_key_weights")
     return out
@@ -420,40 +416,40 @@ def cache_evict(weights, seq_lens, kv_cache, block_tables, out_cache, out_block_
     Returns (out_seq_lens int32 [B], kept int32 [B, budget]: the positions that stay, then -1, out_weights fp32
     [B, budget]: their weights); each is allocated when not given. See include/mla_decode.h.
     """
-    _check_tensors(seq_lens, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens, out_cache=out_cache,
+    _check_tensors(seq_lens, seq_lens=seq_lens, kv_cache=kv_cache, block_tables=block_tables, out_cache=out_cache,
                    out_block_tables=out_block_tables, out_seq_lens=out_seq_lens, kept=kept,
                    device_status=device_status)
-    B, budget = int(seq_lens.numel()), int(budget)
-    if kv_cache.dtype != out_cache.dtype or kv_cache.dim() != 3 or out_cache.dim() != 3 or \
-            kv_cache.shape[2] != 576 or out_cache.shape[1:] != kv_cache.shape[1:]:
+    B, budget, index, dtype = seq_lens.numel(), int(budget), seq_lens.get_device(), kv_cache.dtype
+    if dtype is not out_cache.dtype or kv_cache.dim() != 3 or out_cache.dim() != 3 or kv_cache.size(2) != 576 or \
+            out_cache.size(2) != 576 or out_cache.size(1) != kv_cache.size(1):
         raise ValueError("kv_cache and out_cache must be [pages, 64, 576] of one dtype")
-    if out_block_tables.dtype != torch.int32:
-        raise ValueError("out_block_tables must be int32")
-    if block_tables.dim() != 2 or out_block_tables.dim() != 2 or block_tables.shape[0] != B or \
-            out_block_tables.shape[0] != B or weights.shape[0] != B:
+    if out_block_tables.dtype is not torch.int32 or (device_status is not None and
+                                                     device_status.dtype is not torch.int32):
+        raise ValueError("out_block_tables and device_status must be int32")
+    stride = _weight_rows("weights", weights, index)
+    if block_tables.dim() != 2 or out_block_tables.dim() != 2 or block_tables.size(0) != B or \
+            out_block_tables.size(0) != B or weights.size(0) != B:
         raise ValueError("weights and the block tables must have one row per batch entry")
-    stride = _weight_rows("weights", weights, seq_lens.device)
     if budget < 1:
         raise MlaError(MLA_ERR_INVALID_ARG, "mla_cache_evict")
     if out_seq_lens is None:
         out_seq_lens = torch.empty(B, dtype=torch.int32, device=seq_lens.device)
+    elif out_seq_lens.dtype is not torch.int32 or out_seq_lens.numel() != B:
+        raise ValueError("out_seq_lens must be int32 [batch]")
     if kept is None:
         kept = torch.empty((B, budget), dtype=torch.int32, device=seq_lens.device)
+    elif kept.dtype is not torch.int32 or kept.dim() != 2 or kept.size(0) != B or kept.size(1) != budget:
+        raise ValueError("kept must be int32 [batch, budget]")
     if out_weights is None:
         out_weights = torch.zeros((B, budget), dtype=torch.float32, device=seq_lens.device)
-    if out_seq_lens.dtype != torch.int32 or out_seq_lens.numel() != B:
-        raise ValueError("out_seq_lens must be int32 [batch]")
-    if kept.dtype != torch.int32 or kept.shape != (B, budget):
-        raise ValueError("kept must be int32 [batch, budget]")
-    out_stride = _weight_rows("out_weights", out_weights, seq_lens.device)
-    if out_weights.shape[0] != B or out_weights.shape[1] < budget:
+    out_stride = _weight_rows("out_weights", out_weights, index)
+    if out_weights.size(0) != B or out_weights.size(1) < budget:
         raise ValueError("out_weights must be float32 [batch, >= budget]")
-    rc = _lib.mla_cache_evict(_ptr(weights), stride, int(weights.shape[1]), _ptr(seq_lens), B, budget, int(sinks),
-                              int(recent), _ptr(kv_cache), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
-                              _ptr(block_tables), int(block_tables.shape[1]), _ptr(out_cache),
-                              int(out_cache.shape[0]), _ptr(out_block_tables), int(out_block_tables.shape[1]),
-                              _dtype_code(kv_cache.dtype), _ptr(out_seq_lens), _ptr(kept), _ptr(out_weights),
-                              out_stride, _ptr(device_status), ctypes.c_void_p(_stream_of(seq_lens, stream)))
+    rc = _lib.mla_cache_evict(_ptr(weights), stride, weights.size(1), _ptr(seq_lens), B, budget, int(sinks),
+                              int(recent), _ptr(kv_cache), kv_cache.size(0), kv_cache.size(1), _ptr(block_tables),
+                              block_tables.size(1), _ptr(out_cache), out_cache.size(0), _ptr(out_block_tables),
+                              out_block_tables.size(1), _TORCH_CODES.get(dtype, -1), _ptr(out_seq_lens), _ptr(kept),
+                              _ptr(out_weights), out_stride, _ptr(device_status), _stream_of(seq_lens, stream))
     if rc != 0:
         raise MlaError(rc, "mla_cache_evict")
     return out_seq_lens, kept, out_weights
