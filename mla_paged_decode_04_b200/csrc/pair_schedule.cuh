@@ -73,22 +73,38 @@ __device__ __forceinline__ int tile_weight(const mla_plan& p, const UnitGeom& ug
   return unit_min_keys(p, ug) < kTwoTermKeys ? 3 : 2;
 }
 
-// Tiles of a unit under a window with sinks: those that hold the
-// first keys, then those from the window's first tile on; one run from tile 0
-// when the two meet. sink_tile() maps a unit's i-th tile to its place in the
-// sequence; it is computed again at each use, since the pair kernels have no
-// registers to spare for the map.
-template <int kKeys>
-__device__ __forceinline__ int sink_tile(const mla_plan& p, int klo, int i) {
-  const int nst = (min(p.sinks, klo) + kKeys - 1) / kKeys, tlo = klo / kKeys;
-  return (nst >= tlo || i < nst) ? i : i + tlo - nst;
+// Pages of a unit under a window with sinks: those of the window, then those
+// of the first keys (all from page 0 on, in order, where the two meet). The
+// sinks come last so that a piece's reference maximum comes from whole pages: a
+// few sinks alone in the first tile set one that the next tiles exceed, which
+// costs them the exact order and rescales of O (16 FP8 entries, a window of
+// 8000 keys: 53.7 against @@LAST@@ us). A pair tile of two pages takes two
+// neighbours of this list. sink_page() maps a unit's i-th page to its place in
+// the sequence (past the list: the page behind the last, which no row sees); it
+// is computed again at each use, since the pair kernels have no registers to
+// spare for the map.
+struct SinkPages {
+  int window, first, sinks;  // window pages and the first of them, sink pages
+};
+__device__ __forceinline__ SinkPages sink_pages(const mla_plan& p, int klo, int kend) {
+  SinkPages s;
+  s.first = klo / kTileKeys;
+  s.sinks = (min(p.sinks, klo) + kTileKeys - 1) / kTileKeys;
+  if (s.sinks >= s.first) s.first = s.sinks = 0;
+  s.window = (kend + kTileKeys - 1) / kTileKeys - s.first;
+  return s;
 }
+__device__ __forceinline__ int sink_page(const mla_plan& p, int klo, int kend, int i) {
+  const SinkPages s = sink_pages(p, klo, kend);
+  if (i < s.window) return s.first + i;
+  return i < s.window + s.sinks ? i - s.window : s.first + s.window;
+}
+// Pair tiles of kKeys keys of a unit.
 template <int kKeys, bool kSinks>
 __device__ __forceinline__ int unit_tiles(const mla_plan& p, const UnitGeom& ug) {
-  const int t = unit_span_tiles<kKeys>(ug);
-  if (!kSinks || t == 0) return t;
-  const int nst = (min(p.sinks, ug.klo) + kKeys - 1) / kKeys;
-  return t + min(nst, ug.klo / kKeys);  // (the tiles from 0 on where the two meet)
+  if (!kSinks || ug.kend <= ug.klo) return unit_span_tiles<kKeys>(ug);
+  const SinkPages s = sink_pages(p, ug.klo, ug.kend);
+  return (s.window + s.sinks + kKeys / kTileKeys - 1) / (kKeys / kTileKeys);
 }
 // Whether some row of the unit sees a key of the page at `key` (a multiple of
 // 64), and whether every key of it is seen by some row.

@@ -132,9 +132,9 @@ struct PieceCtx16 {
 #endif
 };
 
-// Place in the sequence of the piece's tile j (sinks).
-__device__ __forceinline__ int piece_tile(const mla_plan& p, const PieceCtx16& c, int j) {
-  return sink_tile<kTile16>(p, c.klo, c.t0 + j);
+// Page of the piece's tile j (sinks).
+__device__ __forceinline__ int piece_page(const mla_plan& p, const PieceCtx16& c, int j) {
+  return sink_page(p, c.klo, c.key1, c.t0 + j);
 }
 
 // Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
@@ -169,8 +169,8 @@ __device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const Pie
   }
 #if MLA_BOUNDS_CHECK
   c.table_ok = c.n_pt <= 0 || (in_bounds(a, c.b, a.plan.batch) &&
-                               in_bounds(a, kSinks ? piece_tile(a.plan, c, 0) : c.page0, a.max_pages_per_seq) &&
-                               in_bounds(a, kSinks ? piece_tile(a.plan, c, c.n_pt - 1) : (int64_t)c.page0 + c.n_pt - 1,
+                               in_bounds(a, kSinks ? piece_page(a.plan, c, 0) : c.page0, a.max_pages_per_seq) &&
+                               in_bounds(a, kSinks ? piece_page(a.plan, c, c.n_pt - 1) : (int64_t)c.page0 + c.n_pt - 1,
                                          a.max_pages_per_seq));
 #endif
   return c;
@@ -183,7 +183,7 @@ __device__ __forceinline__ int piece_entry16(const mla_plan& p, const PieceCtx16
 #if MLA_BOUNDS_CHECK
   if (!c.table_ok) return 0;  // outputs unspecified: MLA_DEV_BOUNDS is set
 #endif
-  return j < c.n_pt ? ld_nc_ordered(c.table + (kSinks ? piece_tile(p, c, j) : c.page0 + j)) : 0;
+  return j < c.n_pt ? ld_nc_ordered(c.table + (kSinks ? piece_page(p, c, j) : c.page0 + j)) : 0;
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page16(const DecodeArgs& a, int pg) {
@@ -272,12 +272,14 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           const int sv = jt % NV;
           const int pg = valid_page16(a, e_nx);
           if (j + 1 < c.n_pt) e_nx = piece_entry16<kSinks>(p, c, j + 1);
+          const bool all_seen =
+              !kSinks || page_all_seen(kTile16 * piece_page(p, c, j), c.klo, c.key1, p.sinks);
           // the scores of the tile exist: its page is in L2 now
           if (!(ok = bounded_wait_cta(bar(L::B_QK_DONE + jt % NQ), (jt / NQ) & 1, abort_flag, a.status))) break;
           if (!(ok = bounded_wait_cta(bar(L::B_V_EMPTY + sv), ((jt / NV) & 1) ^ 1, abort_flag, a.status))) break;
           const uint32_t vs = sb + L::kVOff + sv * L::kVSlot;
           uint32_t full = lead(L::B_V_FULL + sv);
-          if (kSinks && !page_all_seen(kTile16 * piece_tile(p, c, j), c.klo, c.key1, p.sinks)) {
+          if (!all_seen) {
             if (rank == 0) mbar_arrive(bar(L::B_V_FULL + sv));
             full = mapa(bar(L::B_V_LAND + sv), rank);
             mbar_arrive_expect_tx(bar(L::B_V_LAND + sv), L::kVSlot);
@@ -446,6 +448,8 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
         const int ph = (jg >> 1) & 1;
         const int pg_cur = pg_next;
         if (j + 2 < c.n_pt) pg_next = piece_entry16<kSinks>(p, c, j + 2);
+        const int tile_key = kSinks ? kTile16 * piece_page(p, c, j) : c.key0 + kTile16 * j;
+        const bool all_seen = !kSinks || page_all_seen(tile_key, c.klo, c.key1, p.sinks);
         if (!(ok = warp_wait_cta(bar(L::B_S_FULL + buf), ph, abort_flag, a.status))) break;
         tc_fence_after();
         uint32_t sv[32];
@@ -460,13 +464,19 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           page_ok = false;
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
-        const int kb = (kSinks ? kTile16 * piece_tile(p, c, j) : c.key0 + kTile16 * j) + kHalfKeys * hf;
+        const int kb = tile_key + kHalfKeys * hf;
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
-        if (!(page_ok && (kb >= lower || (kSinks && kb + 31 < p.sinks)) && kb + 31 <= limit)) {
+        // (the sinks have a loop of their own, as in the FP8 pair kernel)
+        if (!(page_ok && kb >= lower && kb + 31 <= limit)) {
+          if (kSinks && page_ok && kb < p.sinks) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(page_ok && (kb + i >= lower || (kSinks && kb + i < p.sinks)) && kb + i <= limit))
-              sv[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; ++i)
+              if (kb + i > limit || (kb + i < lower && kb + i >= p.sinks)) sv[i] = __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(page_ok && kb + i >= lower && kb + i <= limit)) sv[i] = __float_as_uint(-INFINITY);
+          }
         }
         float mt;
         {
@@ -590,13 +600,12 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           tmem_wait_st();
         }
         if constexpr (kSinks) {
-          const int kp = kTile16 * piece_tile(p, c, j);
-          if (!page_all_seen(kp, c.klo, c.key1, p.sinks)) {
+          if (!all_seen) {
             const int sv_slot = jg % NV;
             if (!(ok = warp_wait_cta(bar(L::B_V_LAND + sv_slot), (jg / NV) & 1, abort_flag, a.status))) break;
             // one (key, column half) per thread of the group
             const int key = threadIdx.x & 63, h2 = (threadIdx.x >> 6) & 1;
-            if (kp + key >= c.key1 || (kp + key < c.klo && kp + key >= p.sinks)) {
+            if (tile_key + key >= c.key1 || (tile_key + key < c.klo && tile_key + key >= p.sinks)) {
               uint8_t* vrow = smem + L::kVOff + sv_slot * L::kVSlot + h2 * 16384 + key * 128;
 #pragma unroll
               for (int u = 0; u < 16; ++u)

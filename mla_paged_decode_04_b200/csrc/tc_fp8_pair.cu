@@ -181,9 +181,9 @@ struct PieceCtx {
 // faster with it inlined).
 __device__ __noinline__ UnitGeom unit_geom_call(const DecodeArgs& a, int u) { return unit_geom(a, u, false); }
 
-// Place in the sequence of the piece's tile j (sinks).
-__device__ __forceinline__ int piece_tile(const mla_plan& p, const PieceCtx& c, int j) {
-  return sink_tile<kPairTileKeys>(p, c.klo, c.t0 + j);
+// First key of the piece's 64-key tile t (sinks).
+__device__ __forceinline__ int piece_key(const mla_plan& p, const PieceCtx& c, int t) {
+  return kTileKeys * sink_page(p, c.klo, c.key1, 2 * c.t0 + t);
 }
 
 // Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
@@ -238,9 +238,9 @@ template <bool kSinks>
 __device__ __forceinline__ int piece_entry(const DecodeArgs& a, const PieceCtx& c, int t) {
   const mla_plan& p = a.plan;
   if constexpr (kSinks) {
-    // a page that no row sees is not looked up (its V rows are cleared)
-    const int page = 2 * piece_tile(p, c, t >> 1) + (t & 1);
-    if (t >= 2 * c.n_pt || !page_seen(kTileKeys * page, c.klo, c.key1, p.sinks)) return 0;
+    // past the piece or the unit's pages: none is looked up (the V rows are cleared)
+    const int page = sink_page(p, c.klo, c.key1, 2 * c.t0 + t);
+    if (t >= 2 * c.n_pt || kTileKeys * page >= c.key1) return 0;
 #if MLA_BOUNDS_CHECK
     if (!in_bounds(a, c.b, p.batch) || !in_bounds(a, page, a.max_pages_per_seq)) return 0;
 #endif
@@ -250,8 +250,8 @@ __device__ __forceinline__ int piece_entry(const DecodeArgs& a, const PieceCtx& 
 }
 // Whether every key of pair tile j of the piece is seen by some row (sinks).
 __device__ __forceinline__ bool tile_all_seen(const mla_plan& p, const PieceCtx& c, int j) {
-  const int key = kPairTileKeys * piece_tile(p, c, j);
-  return page_all_seen(key, c.klo, c.key1, p.sinks) && page_all_seen(key + kTileKeys, c.klo, c.key1, p.sinks);
+  return page_all_seen(piece_key(p, c, 2 * j), c.klo, c.key1, p.sinks) &&
+         page_all_seen(piece_key(p, c, 2 * j + 1), c.klo, c.key1, p.sinks);
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page(const DecodeArgs& a, int pg) {
@@ -356,12 +356,13 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
             e0_nx = piece_entry<kSinks>(a, c, 2 * (j + 1));
             e1_nx = piece_entry<kSinks>(a, c, 2 * (j + 1) + 1);
           }
+          const bool all_seen = !kSinks || tile_all_seen(p, c, j);
           // the scores of the tile exist: its pages are in L2 now
           if (!(ok = bounded_wait_cta(bar(L::B_QK_DONE + jt % NQ), (jt / NQ) & 1, abort_flag, a.status))) break;
           if (!(ok = bounded_wait_cta(bar(L::B_V_EMPTY + sv), ((jt / NV) & 1) ^ 1, abort_flag, a.status))) break;
           const uint32_t vs = sb + L::kVOff + sv * L::kVSlot;
           uint32_t full = lead(L::B_V_FULL + sv);
-          if (kSinks && !tile_all_seen(p, c, j)) {
+          if (!all_seen) {
             if (rank == 0) mbar_arrive(bar(L::B_V_FULL + sv));
             full = mapa(bar(L::B_V_LAND + sv), rank);
             mbar_arrive_expect_tx(bar(L::B_V_LAND + sv), L::kVSlot);
@@ -477,7 +478,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
     int jt = 0;  // running index of the piece's first tile
 
     for (int k = 0; ok && k < npc; ++k) {
-      const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+      PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
       const bool last_piece = k == npc - 1;
       // causal limit and sliding-window start of this row (rows past the
       // unit compute on whatever Q holds and are never stored)
@@ -552,13 +553,21 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
           page_ok = false;
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
-        const int kb = (kSinks ? kPairTileKeys * piece_tile(p, c, j) : c.key0 + kPairTileKeys * j) + 64 * hf;
+        const int kb = kSinks ? piece_key(p, c, t) : c.key0 + kPairTileKeys * j + 64 * hf;
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
-        if (!(page_ok && (kb >= lower || (kSinks && kb + 63 < p.sinks)) && kb + 63 <= limit)) {
+        // The sinks have a loop of their own: with their term in the common one,
+        // tiles that need no mask at all paid for it too (16 FP8 entries, a
+        // window of 8000 keys: 54.6 against @@MASK@@ us).
+        if (!(page_ok && kb >= lower && kb + 63 <= limit)) {
+          if (kSinks && page_ok && kb < p.sinks) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!(page_ok && (kb + i >= lower || (kSinks && kb + i < p.sinks)) && kb + i <= limit))
-              sv[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 64; ++i)
+              if (kb + i > limit || (kb + i < lower && kb + i >= p.sinks)) sv[i] = __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (!(page_ok && kb + i >= lower && kb + i <= limit)) sv[i] = __float_as_uint(-INFINITY);
+          }
         }
         float mt;
         {
@@ -694,7 +703,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
             const int sv_slot = jg % NV;
             if (!(ok = warp_wait_cta(bar(L::B_V_LAND + sv_slot), (jg / NV) & 1, abort_flag, a.status))) break;
             const int i = threadIdx.x & 127;  // one key of the pair tile per thread of the group
-            const int key = kPairTileKeys * piece_tile(p, c, j) + i;
+            const int key = piece_key(p, c, 2 * j + (i >> 6)) + (i & 63);
             if (key >= c.key1 || (key < c.klo && key >= p.sinks)) {
               uint8_t* vrow = smem + L::kVOff + sv_slot * L::kVSlot + i * 128;  // [half][page][64 keys][128 B]
 #pragma unroll
@@ -719,6 +728,9 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       }
 
       // ---------------------------------------------------------- epilogue of the piece
+      // (sinks: the piece's constants are derived again, since the tile loop has
+      // no registers to carry them)
+      if (kSinks) c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
       // Row sum over both groups and both key halves, relative to the final
       // reference maximum.
       ok = __all_sync(0xffffffffu, ok);

@@ -110,13 +110,17 @@ __device__ __forceinline__ Entry load_entry(const KeyWeightParams& prm, int i, b
   e.klo = a.plan.window > 0 ? max(0, e.n - e.qlen + 1 - a.plan.window) : 0;
   return e;
 }
-// Tiles that hold a key some row sees.
+// Tiles that hold a key some row sees: those of the sinks, then those from
+// the window's first tile on; one run from tile 0 when the two meet.
 __device__ __forceinline__ int entry_tiles(const mla_plan& p, const Entry& e) {
   if (e.n == 0 || e.qlen == 0 || e.klo >= e.n) return 0;
-  UnitGeom ug;
-  ug.klo = e.klo;
-  ug.kend = e.n;
-  return unit_tiles<kTile, true>(p, ug);
+  const int first = e.klo / kTile, nst = (min(plan_has_sinks(p) ? p.sinks : 0, e.klo) + kTile - 1) / kTile;
+  return (e.n + kTile - 1) / kTile - first + min(nst, first);
+}
+// Place in the sequence of an entry's i-th such tile.
+__device__ __forceinline__ int entry_tile(const mla_plan& p, const Entry& e, int i) {
+  const int first = e.klo / kTile, nst = (min(plan_has_sinks(p) ? p.sinks : 0, e.klo) + kTile - 1) / kTile;
+  return (nst >= first || i < nst) ? i : i + first - nst;
 }
 __device__ __forceinline__ int sinks_of(const mla_plan& p) { return plan_has_sinks(p) ? p.sinks : 0; }
 
@@ -143,7 +147,7 @@ struct Walk {
     e = load_entry(prm, i, false);
     return true;
   }
-  __device__ __forceinline__ int tile(const mla_plan& p) const { return sink_tile<kTile>(p, e.klo, idx - start[i]); }
+  __device__ __forceinline__ int tile(const mla_plan& p) const { return entry_tile(p, e, idx - start[i]); }
   // whether this is the last tile of its entry in this pair's run
   __device__ __forceinline__ bool last_of_entry() const { return idx + 1 >= end || idx + 1 >= start[i + 1]; }
 };
