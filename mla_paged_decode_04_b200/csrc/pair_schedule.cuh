@@ -41,6 +41,41 @@ struct SchedInfo {
 constexpr int kMaxSmemPieces = 64;  // pieces a pair keeps in shared memory; the rest go to the spill area
 constexpr uint32_t kSchedBytes = 1024;
 static_assert(kMaxSmemPieces * sizeof(Piece) + sizeof(SchedInfo) <= kSchedBytes, "schedule area");
+// Geometry of the units of a pair's first pieces, beside the piece list (plans
+// with sinks, whose units are short): with it a role begins a piece without a
+// global load (seq_lens, and cu_q for ragged queries: 2200 of a piece's 38,000
+// cycles; ragged FP8 prefill, window 1024: 560 -> 520 us). Later pieces derive
+// it again. Plans without sinks do so always: their units are long, and with the
+// branch in every role the ragged FP8 prefill of 512 to 4096 new tokens took
+// 7.07 instead of 6.87 ms.
+struct PieceGeo {
+  int b, nq, rows, klo, kend;
+  uint32_t row0_lo, row0_hi;
+};
+constexpr int kMaxPieceGeo = 32;
+constexpr uint32_t kPieceGeoBytes = kMaxPieceGeo * sizeof(PieceGeo);
+__device__ __forceinline__ void store_geo(PieceGeo* g, const UnitGeom& ug) {
+  g->b = ug.b;
+  g->nq = ug.nq;
+  g->rows = ug.rows;
+  g->klo = ug.klo;
+  g->kend = ug.kend;
+  g->row0_lo = (uint32_t)ug.row0;
+  g->row0_hi = (uint32_t)((uint64_t)ug.row0 >> 32);
+}
+// (group and n are not kept: no role needs them)
+__device__ __forceinline__ UnitGeom load_geo(const PieceGeo* g) {
+  UnitGeom ug;
+  ug.b = g->b;
+  ug.g = 0;
+  ug.n = 0;
+  ug.nq = g->nq;
+  ug.rows = g->rows;
+  ug.klo = g->klo;
+  ug.kend = g->kend;
+  ug.row0 = (int64_t)(((uint64_t)g->row0_hi << 32) | g->row0_lo);
+  return ug;
+}
 constexpr int kMinPairWeight = 4;  // pairs get at least this much weight (>= the heaviest tile)
 
 // Unit at schedule slot s, and the slot of unit u (u = entry * G + group).
@@ -78,11 +113,8 @@ __device__ __forceinline__ int tile_weight(const mla_plan& p, const UnitGeom& ug
 // sinks come last so that a piece's reference maximum comes from whole pages: a
 // few sinks alone in the first tile set one that the next tiles exceed, which
 // costs them the exact order and rescales of O (16 FP8 entries, a window of
-// 8000 keys: 53.7 against @@LAST@@ us). A pair tile of two pages takes two
-// neighbours of this list. sink_page() maps a unit's i-th page to its place in
-// the sequence (past the list: the page behind the last, which no row sees); it
-// is computed again at each use, since the pair kernels have no registers to
-// spare for the map.
+// 8000 keys: 53.7 against 45.0 us). A pair tile of two pages takes two
+// neighbours of this list.
 struct SinkPages {
   int window, first, sinks;  // window pages and the first of them, sink pages
 };
@@ -94,10 +126,17 @@ __device__ __forceinline__ SinkPages sink_pages(const mla_plan& p, int klo, int 
   s.window = (kend + kTileKeys - 1) / kTileKeys - s.first;
   return s;
 }
-__device__ __forceinline__ int sink_page(const mla_plan& p, int klo, int kend, int i) {
+// The pages of a piece that begins `skip` pages into its unit: page i is
+// base + i before `left`, then the sinks' from 0 on. (An FP8 unit of an odd
+// number of pages ends half a tile past the list, at pages `end` on, which no row
+// sees.)
+struct PiecePages {
+  int base, left, end;
+  __device__ __forceinline__ int operator()(int i) const { return i < left ? base + i : i - left; }
+};
+__device__ __forceinline__ PiecePages piece_pages(const mla_plan& p, int klo, int kend, int skip) {
   const SinkPages s = sink_pages(p, klo, kend);
-  if (i < s.window) return s.first + i;
-  return i < s.window + s.sinks ? i - s.window : s.first + s.window;
+  return PiecePages{s.first + skip, s.window - skip, s.window + s.sinks - skip};
 }
 // Pair tiles of kKeys keys of a unit.
 template <int kKeys, bool kSinks>
@@ -153,7 +192,7 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
 // spill area (read back by load_piece). CTA 0 of pair 0 also writes the slot
 // start table the combine reads, then its ready flag.
 template <int kKeys, bool kSinks = false>
-__device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uint8_t* sched_area) {
+__device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uint8_t* sched_area, PieceGeo* geo) {
   const mla_plan& p = a.plan;
   Piece* smem_list = reinterpret_cast<Piece*>(sched_area);
   SchedInfo* info = reinterpret_cast<SchedInfo*>(sched_area + kMaxSmemPieces * sizeof(Piece));
@@ -168,6 +207,7 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
   // them from the first scan (a plan of at most one slot per thread reads
   // seq_lens once); the others read them again.
   int t_beg = 0, w_beg = 2;
+  UnitGeom g_beg{};
   auto geometry = [&](int sl, int& t, int& w) {
     if (sl == s_beg) {
       t = t_beg, w = w_beg;
@@ -181,7 +221,7 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
   for (int sl = s_beg; sl < s_end; ++sl) {
     const UnitGeom ug = unit_geom(a, sched_unit(p, sl), writer);
     const int t = unit_tiles<kKeys, kSinks>(p, ug), w = tile_weight<kSinks>(p, ug);
-    if (sl == s_beg) t_beg = t, w_beg = w;
+    if (sl == s_beg) t_beg = t, w_beg = w, g_beg = ug;
     run += unit_lead_weight(t) + t * w;
   }
   int incl = warp_incl_scan(run);
@@ -268,6 +308,7 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
         pc.t0 = i0;
         pc.t1 = i1;
         if (k < kMaxSmemPieces) smem_list[k] = pc;
+        if (kSinks && k < kMaxPieceGeo) store_geo(geo + k, sl == s_beg ? g_beg : unit_geom(a, u, false));
         if (spill && in_bounds(a, spill_base + k, spill_entries(a))) spill[k] = pc;
         ++k;
       }

@@ -93,7 +93,8 @@ struct Layout16 {
   static constexpr uint32_t kMiscOff = kBarOff + 512;
   // The dynamic shared memory base is 1024-aligned (checked at run time;
   // the kernel refuses to run otherwise), so no alignment slack is added.
-  static constexpr uint32_t kSmemBytes = kMiscOff + 16;
+  static constexpr uint32_t kGeoOff = kMiscOff + 16;  // geometry of the first pieces
+  static constexpr uint32_t kSmemBytes = kGeoOff + kPieceGeoBytes;
   static_assert(kQRes % 1024 == 0 && kPOff % 1024 == 0 && kKOff % 1024 == 0 && kVOff % 1024 == 0, "alignment");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   // the last piece's epilogue stages the 64 x 512 fp32 output tile in the
@@ -120,22 +121,17 @@ struct Pair16Params {
 
 // Per-piece constants every role derives the same way.
 struct PieceCtx16 {
-  int b, g, n, nq, rows, key0, key1, n_pt, page0;
+  int b, nq, rows, key0, key1, n_pt, page0;
   int64_t row0;
   const int32_t* table;
   bool whole;  // the piece is the whole unit: final output, not a partial
   bool cont;   // the piece begins inside its unit (the pair's first piece)
   int klo;  // with sinks: the window's first key (key1: the unit's end)
-  int t0;   // first tile of the piece within its unit
+  PiecePages at;
 #if MLA_BOUNDS_CHECK
   bool table_ok;  // the piece's block-table entries lie inside row b of the table
 #endif
 };
-
-// Page of the piece's tile j (sinks).
-__device__ __forceinline__ int piece_page(const mla_plan& p, const PieceCtx16& c, int j) {
-  return sink_page(p, c.klo, c.key1, c.t0 + j);
-}
 
 // Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
 // V rows of a tile that no row of the unit sees (past the sequence's end, or
@@ -144,12 +140,13 @@ __device__ __forceinline__ int piece_page(const mla_plan& p, const PieceCtx16& c
 // the leader's V_FULL; the softmax group that writes the tile's P waits for it,
 // clears the rows and hands both over with P_FULL.
 template <bool kSinks>
-__device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const Piece& pc) {
+__device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const uint8_t* smem, int k) {
   PieceCtx16 c;
-  const UnitGeom ug = unit_geom(a, pc.u, false);
+  const Piece pc = load_piece(a, smem, k);
+  const UnitGeom ug = kSinks && k < kMaxPieceGeo
+                          ? load_geo(reinterpret_cast<const PieceGeo*>(smem + Layout16::kGeoOff) + k)
+                          : unit_geom(a, pc.u, false);
   c.b = ug.b;
-  c.g = ug.g;
-  c.n = ug.n;
   c.nq = ug.nq;
   c.rows = ug.rows;
   const int tlo = ug.klo / kTile16;  // the unit's first page
@@ -162,15 +159,15 @@ __device__ __forceinline__ PieceCtx16 piece_ctx16(const DecodeArgs& a, const Pie
   c.whole = pc.t0 == 0 && c.key1 >= ug.kend;
   c.cont = pc.t0 > 0;
   c.klo = ug.klo;
-  c.t0 = pc.t0;
   if constexpr (kSinks) {
+    c.at = piece_pages(a.plan, ug.klo, ug.kend, pc.t0);
     c.key1 = ug.kend;
     c.whole = pc.t0 == 0 && pc.t1 == unit_tiles<kTile16, true>(a.plan, ug);
   }
 #if MLA_BOUNDS_CHECK
   c.table_ok = c.n_pt <= 0 || (in_bounds(a, c.b, a.plan.batch) &&
-                               in_bounds(a, kSinks ? piece_page(a.plan, c, 0) : c.page0, a.max_pages_per_seq) &&
-                               in_bounds(a, kSinks ? piece_page(a.plan, c, c.n_pt - 1) : (int64_t)c.page0 + c.n_pt - 1,
+                               in_bounds(a, kSinks ? c.at(0) : c.page0, a.max_pages_per_seq) &&
+                               in_bounds(a, kSinks ? c.at(c.n_pt - 1) : (int64_t)c.page0 + c.n_pt - 1,
                                          a.max_pages_per_seq));
 #endif
   return c;
@@ -183,7 +180,7 @@ __device__ __forceinline__ int piece_entry16(const mla_plan& p, const PieceCtx16
 #if MLA_BOUNDS_CHECK
   if (!c.table_ok) return 0;  // outputs unspecified: MLA_DEV_BOUNDS is set
 #endif
-  return j < c.n_pt ? ld_nc_ordered(c.table + (kSinks ? piece_page(p, c, j) : c.page0 + j)) : 0;
+  return j < c.n_pt ? ld_nc_ordered(c.table + (kSinks ? c.at(j) : c.page0 + j)) : 0;
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page16(const DecodeArgs& a, int pg) {
@@ -226,7 +223,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
+        const PieceCtx16 c = piece_ctx16<kSinks>(a, smem, k);
         if (k > 0) {
           // the Q areas and the staging slots are free once every MMA of the
           // previous piece is done: its O_FINAL phase
@@ -266,14 +263,14 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
+        const PieceCtx16 c = piece_ctx16<kSinks>(a, smem, k);
         int e_nx = piece_entry16<kSinks>(p, c, 0);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sv = jt % NV;
           const int pg = valid_page16(a, e_nx);
           if (j + 1 < c.n_pt) e_nx = piece_entry16<kSinks>(p, c, j + 1);
           const bool all_seen =
-              !kSinks || page_all_seen(kTile16 * piece_page(p, c, j), c.klo, c.key1, p.sinks);
+              !kSinks || page_all_seen(kTile16 * c.at(j), c.klo, c.key1, p.sinks);
           // the scores of the tile exist: its page is in L2 now
           if (!(ok = bounded_wait_cta(bar(L::B_QK_DONE + jt % NQ), (jt / NQ) & 1, abort_flag, a.status))) break;
           if (!(ok = bounded_wait_cta(bar(L::B_V_EMPTY + sv), ((jt / NV) & 1) ^ 1, abort_flag, a.status))) break;
@@ -398,12 +395,12 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
     int jt = 0;  // running index of the piece's first tile
 
     for (int k = 0; ok && k < npc; ++k) {
-      const PieceCtx16 c = piece_ctx16<kSinks>(a, load_piece(a, smem, k));
+      const PieceCtx16 c = piece_ctx16<kSinks>(a, smem, k);
       const bool last_piece = k == npc - 1;
       // causal limit and sliding-window start of this row (rows past the
       // unit compute on whatever Q holds and are never stored)
       const int limit = (r < c.rows) ? min(c.nq + r / H, c.key1 - 1) : c.key1 - 1;
-      const int lower = (r < c.rows) ? row_key_lo(p, c.nq + r / H) : 0;
+      const int row_lower = (!kSinks && r < c.rows) ? row_key_lo(p, c.nq + r / H) : 0;
 
       // Q dims 0..255 (and, group 0, the rope) of local row rl into TMEM:
       // lane quarters q and q^2 both hold rows 32(q%2)..; group g copies
@@ -448,7 +445,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
         const int ph = (jg >> 1) & 1;
         const int pg_cur = pg_next;
         if (j + 2 < c.n_pt) pg_next = piece_entry16<kSinks>(p, c, j + 2);
-        const int tile_key = kSinks ? kTile16 * piece_page(p, c, j) : c.key0 + kTile16 * j;
+        const int tile_key = kSinks ? kTile16 * c.at(j) : c.key0 + kTile16 * j;
         const bool all_seen = !kSinks || page_all_seen(tile_key, c.klo, c.key1, p.sinks);
         if (!(ok = warp_wait_cta(bar(L::B_S_FULL + buf), ph, abort_flag, a.status))) break;
         tc_fence_after();
@@ -465,6 +462,7 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
         const int kb = tile_key + kHalfKeys * hf;
+        const int lower = kSinks ? limit + 1 - p.window : row_lower;  // (no register to spare for it)
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
         // (the sinks have a loop of their own, as in the FP8 pair kernel)
         if (!(page_ok && kb >= lower && kb + 31 <= limit)) {
@@ -674,12 +672,10 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
           uint32_t o[32];
           tmem_ld32(tmem + tl + kOCol + 128u * grp + 32u * cc, o);
           tmem_wait_ld();
-          if (r >= c.rows) continue;
           const int col = 256 * grp + 128 * hf + 32 * cc;
-          if (c.whole ? !in_bounds(a, c.row0 + r, out_rows(a)) : !in_bounds(a, slot * M + r, balanced_slots(a) * M))
-            continue;
+          if (!kSinks && r >= c.rows) continue;
           if (c.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (c.row0 + r) * MLA_D_V + col);
+            uint4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
@@ -690,9 +686,22 @@ __device__ __forceinline__ void pair_cta16(const Pair16Params& prm, uint8_t* sme
                 __nv_bfloat162 h2 = __floats2bfloat162_rn(f0, f1);
                 pk[e] = *reinterpret_cast<uint32_t*>(&h2);
               }
-              dst[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              v[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-          } else {
+            // Sinks, whose units are short: a quad of lanes stores its four rows
+            // one after the other, 64 bytes each, so that a warp's store touches 8
+            // rows instead of 32 (ragged FP8 prefill, window 1024: 521 -> 499 us).
+            // The other plans' loops lose more to the added code than they gain
+            // (128 entries of lognormal lengths, 256 rows: 1.48 -> 1.53 ms).
+            if constexpr (kSinks) quad_transpose(v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int ru = kSinks ? (r & ~3) + u : r;
+              if (ru >= c.rows || !in_bounds(a, c.row0 + ru, out_rows(a))) continue;
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (c.row0 + ru) * MLA_D_V + col +
+                                        8 * (kSinks ? (lane & 3) : u)) = v[u];
+            }
+          } else if (r < c.rows && in_bounds(a, slot * M + r, balanced_slots(a) * M)) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int64_t c4 = col / 4 + u;  // 16-byte column chunk
@@ -904,7 +913,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The combine grid may now start (the unit counters and the table's ready
   // flag it waits on are cleared) and take the SMs of pairs that finish early.
   launch_dependents();
-  build_schedule<kTile16, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
+  build_schedule<kTile16, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem,
+                                  reinterpret_cast<PieceGeo*>(smem + Layout16::kGeoOff));  // every thread
   __syncthreads();
   const int npc = info->npc;
   if (npc == 0) {  // no work for this pair (the same in both CTAs)

@@ -144,6 +144,27 @@ __device__ __forceinline__ void drain_pair_commits(uint32_t bar0, int lane, int 
   if (t >= 0) drain_phase(bar0 + 8u * (uint32_t)(b + t % n), (uint32_t)(t / n) & 1);
 }
 
+// Four lanes (a quad) hold four 16-byte chunks each, lane i those of row i;
+// afterwards lane i holds chunk i of the four rows, so that a quad's stores are
+// 64 contiguous bytes. Two exchange steps of a 4 x 4 transposition; every lane of
+// the warp takes part.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto exchange = [&](uint4& a, uint4& b, int bit) {
+    const bool upper = lane & bit;  // keeps b, gets the partner's b as a; the lower lane the other way round
+    uint4 send = upper ? a : b;
+    send.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+    send.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+    send.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+    send.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+    if (upper) a = send; else b = send;
+  };
+  exchange(v[0], v[1], 1);
+  exchange(v[2], v[3], 1);
+  exchange(v[0], v[2], 2);
+  exchange(v[1], v[3], 2);
+}
+
 // Write 32 output columns [col, col + 32) of flat row `rg`: BF16 to `out`
 // when there is one split, else fp32 to the split's partial. inv = 0 means the
 // row saw no key (written as exact zeros).

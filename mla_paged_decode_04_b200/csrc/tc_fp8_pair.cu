@@ -85,6 +85,8 @@ constexpr float kSigma = 4.f;        // P <= 2^(kTau + kSigma) = 256 <= 448
 // with it the layout) is known.
 constexpr uint32_t kPairBarOff = kSchedBytes;        // 64 mbarriers
 constexpr uint32_t kPairMiscOff = kPairBarOff + 512;  // TMEM address, abort flag
+constexpr uint32_t kPairGeoOff = kPairMiscOff + 512;  // geometry of the first pieces
+static_assert(kPieceGeoBytes <= 1024, "geometry area");
 
 template <bool kTwo>
 struct PairLayout {
@@ -92,7 +94,7 @@ struct PairLayout {
   static constexpr int NV = 2;                                  // V-ring slots: 256 V columns of both pages
   static constexpr uint32_t kBarOff = kPairBarOff;
   static constexpr uint32_t kMiscOff = kPairMiscOff;
-  static constexpr uint32_t kQRope = kMiscOff + 512;            // 64 rows x 64 B (SW64)
+  static constexpr uint32_t kQRope = kPairGeoOff + 1024;        // 64 rows x 64 B (SW64)
   static constexpr uint32_t kPPlane = 64 * 128;                 // 64 rows x 128 keys E4M3 (SW128)
   static constexpr uint32_t kPBuf = (kTwo ? 2 : 1) * kPPlane;   // hi (and lo) plane
   static constexpr uint32_t kPOff = kQRope + 4096;              // P[2 buffers] (1024-aligned)
@@ -165,14 +167,14 @@ struct PairParams {
 
 // Per-piece constants every role derives the same way.
 struct PieceCtx {
-  int b, g, n, nq, rows, key0, key1, n_pt, n_tiles, tile0;
+  int b, nq, rows, key0, key1, n_pt, n_tiles, tile0;
   int64_t row0;
   const int32_t* table;
   bool whole;  // the piece is the whole unit: final output, not a partial
   bool cont;   // the piece begins inside its unit (the pair's first piece)
   bool two;    // two-term P
   int klo;  // with sinks: the window's first key (key1: the unit's end)
-  int t0;   // first tile of the piece within its unit
+  PiecePages at;
 };
 
 // The unit geometry as a call, not inlined into every role: the roles' code
@@ -181,9 +183,9 @@ struct PieceCtx {
 // faster with it inlined).
 __device__ __noinline__ UnitGeom unit_geom_call(const DecodeArgs& a, int u) { return unit_geom(a, u, false); }
 
-// First key of the piece's 64-key tile t (sinks).
-__device__ __forceinline__ int piece_key(const mla_plan& p, const PieceCtx& c, int t) {
-  return kTileKeys * sink_page(p, c.klo, c.key1, 2 * c.t0 + t);
+// First key of the piece's 64-key tile t (sinks; past the unit's pages its end).
+__device__ __forceinline__ int piece_key(const PieceCtx& c, int t) {
+  return t < c.at.end ? kTileKeys * c.at(t) : c.key1;
 }
 
 // Masked keys weigh nothing in P, but 0 times a NaN is a NaN: with sinks, the
@@ -193,13 +195,14 @@ __device__ __forceinline__ int piece_key(const mla_plan& p, const PieceCtx& c, i
 // the leader's V_FULL; the softmax group that writes the tile's P waits for it,
 // clears the rows and hands both over with P_FULL.
 template <bool kSinks>
-__device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& pc, bool kTwo) {
+__device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const uint8_t* smem, int k, bool kTwo) {
   const mla_plan& p = a.plan;
   PieceCtx c;
-  const UnitGeom ug = unit_geom_call(a, pc.u);
+  const Piece pc = load_piece(a, smem, k);
+  const UnitGeom ug = kSinks && k < kMaxPieceGeo
+                          ? load_geo(reinterpret_cast<const PieceGeo*>(smem + kPairGeoOff) + k)
+                          : unit_geom_call(a, pc.u);
   c.b = ug.b;
-  c.g = ug.g;
-  c.n = ug.n;
   c.nq = ug.nq;
   c.rows = ug.rows;
   const int tlo = ug.klo / kPairTileKeys;  // the unit's first pair tile
@@ -215,8 +218,8 @@ __device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& 
   c.cont = pc.t0 > 0;
   c.two = kTwo && tile_weight<kSinks>(p, ug) == 3;  // the same rule as the schedule's weights
   c.klo = ug.klo;
-  c.t0 = pc.t0;
   if constexpr (kSinks) {
+    c.at = piece_pages(p, ug.klo, ug.kend, 2 * pc.t0);
     c.key1 = ug.kend;
     c.whole = pc.t0 == 0 && pc.t1 == unit_tiles<kPairTileKeys, true>(p, ug);
     return c;
@@ -236,13 +239,13 @@ __device__ __forceinline__ PieceCtx piece_ctx(const DecodeArgs& a, const Piece& 
 // checked after it, so its latency stays off the ring's critical path.
 template <bool kSinks>
 __device__ __forceinline__ int piece_entry(const DecodeArgs& a, const PieceCtx& c, int t) {
-  const mla_plan& p = a.plan;
+  (void)a;
   if constexpr (kSinks) {
     // past the piece or the unit's pages: none is looked up (the V rows are cleared)
-    const int page = sink_page(p, c.klo, c.key1, 2 * c.t0 + t);
-    if (t >= 2 * c.n_pt || kTileKeys * page >= c.key1) return 0;
+    if (t >= 2 * c.n_pt || t >= c.at.end) return 0;
+    const int page = c.at(t);
 #if MLA_BOUNDS_CHECK
-    if (!in_bounds(a, c.b, p.batch) || !in_bounds(a, page, a.max_pages_per_seq)) return 0;
+    if (!in_bounds(a, c.b, a.plan.batch) || !in_bounds(a, page, a.max_pages_per_seq)) return 0;
 #endif
     return ld_nc_ordered(c.table + page);
   }
@@ -250,8 +253,8 @@ __device__ __forceinline__ int piece_entry(const DecodeArgs& a, const PieceCtx& 
 }
 // Whether every key of pair tile j of the piece is seen by some row (sinks).
 __device__ __forceinline__ bool tile_all_seen(const mla_plan& p, const PieceCtx& c, int j) {
-  return page_all_seen(piece_key(p, c, 2 * j), c.klo, c.key1, p.sinks) &&
-         page_all_seen(piece_key(p, c, 2 * j + 1), c.klo, c.key1, p.sinks);
+  return page_all_seen(piece_key(c, 2 * j), c.klo, c.key1, p.sinks) &&
+         page_all_seen(piece_key(c, 2 * j + 1), c.klo, c.key1, p.sinks);
 }
 // an entry outside the cache reads page 0 (its keys are masked by the softmax)
 __device__ __forceinline__ int valid_page(const DecodeArgs& a, int pg) {
@@ -302,7 +305,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;     // tile counter across pieces
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+        const PieceCtx c = piece_ctx<kSinks>(a, smem, k, kTwo);
         if (k > 0) {
           // Q rope, Q in TMEM and the staging slot are free once every MMA of
           // the previous piece is done: its O_FINAL phase. (The V ring's own
@@ -347,7 +350,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+        const PieceCtx c = piece_ctx<kSinks>(a, smem, k, kTwo);
         int e0_nx = piece_entry<kSinks>(a, c, 0), e1_nx = piece_entry<kSinks>(a, c, 1);
         for (int j = 0; j < c.n_pt; ++j, ++jt) {
           const int sv = jt % NV;
@@ -426,7 +429,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       int jt = 0;
       bool ok = true;
       for (int k = 0; ok && k < npc; ++k) {
-        const PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+        const PieceCtx c = piece_ctx<kSinks>(a, smem, k, kTwo);
         // the piece's first P.V overwrites O: the previous piece's epilogue
         // must have read it
         if (k > 0 && !(ok = warp_wait(bar(L::B_O_FREE), (k - 1) & 1, abort_flag, a.status))) break;
@@ -478,12 +481,12 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
     int jt = 0;  // running index of the piece's first tile
 
     for (int k = 0; ok && k < npc; ++k) {
-      PieceCtx c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+      PieceCtx c = piece_ctx<kSinks>(a, smem, k, kTwo);
       const bool last_piece = k == npc - 1;
       // causal limit and sliding-window start of this row (rows past the
       // unit compute on whatever Q holds and are never stored)
       const int limit = (r < c.rows) ? min(c.nq + r / H, c.key1 - 1) : c.key1 - 1;
-      const int lower = (r < c.rows) ? row_key_lo(p, c.nq + r / H) : 0;
+      const int row_lower = (!kSinks && r < c.rows) ? row_key_lo(p, c.nq + r / H) : 0;
 
       // Q latent dims of local row rl into TMEM (A operand of S = Q.K^T): lane
       // quarters q and q^2 both hold rows 32(q%2)..; group g copies chunks
@@ -553,11 +556,12 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
           page_ok = false;
           if (lane == 0 && (q & 1) == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
         }
-        const int kb = kSinks ? piece_key(p, c, t) : c.key0 + kPairTileKeys * j + 64 * hf;
+        const int kb = kSinks ? piece_key(c, t) : c.key0 + kPairTileKeys * j + 64 * hf;
+        const int lower = kSinks ? limit + 1 - p.window : row_lower;  // (no register to spare for it)
         // raw scores; masked keys become -inf (sl2 > 0, so max commutes with the scale)
-        // The sinks have a loop of their own: with their term in the common one,
-        // tiles that need no mask at all paid for it too (16 FP8 entries, a
-        // window of 8000 keys: 54.6 against @@MASK@@ us).
+        // The sinks have a loop of their own: with their term in the common one
+        // the masks cost every boundary tile more (ragged FP8 prefill, window 1024:
+        // 706 -> 667 us).
         if (!(page_ok && kb >= lower && kb + 63 <= limit)) {
           if (kSinks && page_ok && kb < p.sinks) {
 #pragma unroll
@@ -703,7 +707,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
             const int sv_slot = jg % NV;
             if (!(ok = warp_wait_cta(bar(L::B_V_LAND + sv_slot), (jg / NV) & 1, abort_flag, a.status))) break;
             const int i = threadIdx.x & 127;  // one key of the pair tile per thread of the group
-            const int key = piece_key(p, c, 2 * j + (i >> 6)) + (i & 63);
+            const int key = piece_key(c, 2 * j + (i >> 6)) + (i & 63);
             if (key >= c.key1 || (key < c.klo && key >= p.sinks)) {
               uint8_t* vrow = smem + L::kVOff + sv_slot * L::kVSlot + i * 128;  // [half][page][64 keys][128 B]
 #pragma unroll
@@ -730,7 +734,7 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
       // ---------------------------------------------------------- epilogue of the piece
       // (sinks: the piece's constants are derived again, since the tile loop has
       // no registers to carry them)
-      if (kSinks) c = piece_ctx<kSinks>(a, load_piece(a, smem, k), kTwo);
+      if (kSinks) c = piece_ctx<kSinks>(a, smem, k, kTwo);
       // Row sum over both groups and both key halves, relative to the final
       // reference maximum.
       ok = __all_sync(0xffffffffu, ok);
@@ -779,12 +783,10 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
           uint32_t o[32];
           tmem_ld32(tmem + tl + kOCol + 128u * grp + 32u * cc, o);
           tmem_wait_ld();
-          if (r >= c.rows) continue;
           const int col = 256 * grp + 128 * hf + 32 * cc;
-          if (c.whole ? !in_bounds(a, c.row0 + r, out_rows(a)) : !in_bounds(a, slot * M + r, balanced_slots(a) * M))
-            continue;
+          if (!kSinks && r >= c.rows) continue;
           if (c.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (c.row0 + r) * MLA_D_V + col);
+            uint4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
@@ -795,9 +797,22 @@ __device__ __forceinline__ void pair_cta(const PairParams& prm, uint8_t* smem, i
                 __nv_bfloat162 h2 = __floats2bfloat162_rn(f0, f1);
                 pk[e] = *reinterpret_cast<uint32_t*>(&h2);
               }
-              dst[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              v[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-          } else {
+            // Sinks, whose units are short: a quad of lanes stores its four rows
+            // one after the other, 64 bytes each, so that a warp's store touches 8
+            // rows instead of 32 (ragged FP8 prefill, window 1024: 521 -> 499 us).
+            // The other plans' loops lose more to the added code than they gain
+            // (128 entries of lognormal lengths, 256 rows: 1.48 -> 1.53 ms).
+            if constexpr (kSinks) quad_transpose(v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int ru = kSinks ? (r & ~3) + u : r;
+              if (ru >= c.rows || !in_bounds(a, c.row0 + ru, out_rows(a))) continue;
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (c.row0 + ru) * MLA_D_V + col +
+                                        8 * (kSinks ? (lane & 3) : u)) = v[u];
+            }
+          } else if (r < c.rows && in_bounds(a, slot * M + r, balanced_slots(a) * M)) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int64_t c4 = col / 4 + u;  // 16-byte column chunk
@@ -1002,7 +1017,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The combine grid may now start (the unit counters and the table's ready
   // flag it waits on are cleared) and take the SMs of pairs that finish early.
   launch_dependents();
-  build_schedule<kPairTileKeys, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem);  // every thread
+  build_schedule<kPairTileKeys, kSinks>(prm.a, blockIdx.x >> 1, cluster_ctarank(), smem,
+                                        reinterpret_cast<PieceGeo*>(smem + kPairGeoOff));  // every thread
   __syncthreads();
   const int npc = info->npc;
   if (npc == 0) {  // no work for this pair (the same in both CTAs)
