@@ -56,14 +56,15 @@ constexpr int kTile = 256;       // keys per pair tile
 constexpr int kHalf = 128;       // keys of a tile per CTA
 constexpr int kThreads = 384;
 enum Form { kRowsStay = 0, kKeysStay = 1, kBothStream = 2 };
-constexpr int kMaxEntries = 2048;  // entries of one launch: their tile counts are kept in shared memory
+constexpr int kMaxEntries = 1024;  // entries of one launch: their tiles and lengths are kept in shared memory
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlots = 9;     // ring slots a tile is cut into
 constexpr uint32_t kChunkBytes = 128 * 128;
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kStartOff = 0;                                   // int [kMaxEntries + 1]: first tile of an entry
-constexpr uint32_t kLseOff = kStartOff + 8448;                      // float [group][2][256]: -lse * log2(e)
+constexpr uint32_t kLenOff = kStartOff + 4 * (kMaxEntries + 32);   // int [kMaxEntries]: keys of an entry
+constexpr uint32_t kLseOff = kLenOff + 4 * kMaxEntries;                     // float [group][2][256]: -lse * log2(e)
 constexpr uint32_t kLastOff = kLseOff + 4096;                       // int [group][2][256]: newest key of the row
 constexpr uint32_t kSumOff = kLastOff + 4096;                       // float [128]: group 1's sums
 constexpr uint32_t kScanOff = kSumOff + 512;                        // int [12]
@@ -98,11 +99,11 @@ struct Entry {
   int b, n, qlen, rows, klo;
   int64_t q0;
 };
-__device__ __forceinline__ Entry load_entry(const KeyWeightParams& prm, int i, bool flag) {
+__device__ __forceinline__ Entry make_entry(const KeyWeightParams& prm, int i, int n, bool flag) {
   const DecodeArgs& a = prm.k.a;
   Entry e;
   e.b = prm.b0 + i;
-  e.n = effective_seq_len(a, e.b, flag);
+  e.n = n;
   const EntryQ q = entry_q(a, e.b, flag);
   e.q0 = q.q0;
   e.qlen = q.qlen;
@@ -126,11 +127,12 @@ __device__ __forceinline__ int sinks_of(const mla_plan& p) { return plan_has_sin
 
 // The tiles of this pair, in the order every role walks them.
 struct Walk {
-  const int* start;  // [nb + 1]
+  const int *start, *len;  // [nb + 1], [nb]
   int idx, end, step, i;
   Entry e;
   __device__ __forceinline__ Walk(const KeyWeightParams& prm, const uint8_t* smem, bool groups) {
     start = reinterpret_cast<const int*>(smem + kStartOff);
+    len = reinterpret_cast<const int*>(smem + kLenOff);
     const int64_t total = start[prm.nb];
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     idx = groups ? pair : (int)(total * pair / pairs);
@@ -144,7 +146,7 @@ struct Walk {
     if (i >= 0 && idx < start[i + 1]) return false;
     do ++i;
     while (idx >= start[i + 1]);
-    e = load_entry(prm, i, false);
+    e = make_entry(prm, i, len[i], false);
     return true;
   }
   __device__ __forceinline__ int tile(const mla_plan& p) const { return entry_tile(p, e, idx - start[i]); }
@@ -231,17 +233,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t res_slot = kStays ? (uint32_t)res_rows * 128u : 0u;  // bytes of a resident chunk's place
   const uint32_t ring0 = (res0 + C::kChunks * res_slot + 1023u) & ~1023u;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      int count = 1;
-      if (i >= B_S_EMPTY && i < B_S_EMPTY + 2) count = 8;      // a group's warps in both CTAs
-      if (i >= B_LSE) count = 4;                               // a group's warps
-      mbar_init(bar(i), (uint32_t)count);
-    }
-    *abort_flag = 0;
-    issued[0] = issued[1] = 0;
+  if (threadIdx.x < kNumBars) {
+    const int i = threadIdx.x;
+    // S_EMPTY: a sum group's warps in both CTAs; from LSE on a group's warps
+    mbar_init(bar(i), (i >= B_S_EMPTY && i < B_S_EMPTY + 2) ? 8u : i >= B_LSE ? 4u : 1u);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) *abort_flag = issued[0] = issued[1] = 0;
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
@@ -260,13 +258,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // first tile of every entry: thread runs, a scan over the block
   {
     int* start = reinterpret_cast<int*>(smem + kStartOff);
+    int* len = reinterpret_cast<int*>(smem + kLenOff);
     int* scan = reinterpret_cast<int*>(smem + kScanOff);
     const int per = (prm.nb + kThreads - 1) / kThreads;
     const int i0 = min(prm.nb, (int)threadIdx.x * per), i1 = min(prm.nb, i0 + per);
     int run = 0;
     for (int i = i0; i < i1; ++i) {
+      const int n = effective_seq_len(a, prm.b0 + i, blockIdx.x == 0);
       start[i] = run;
-      run += entry_tiles(p, load_entry(prm, i, blockIdx.x == 0));
+      len[i] = n;
+      run += entry_tiles(p, make_entry(prm, i, n, blockIdx.x == 0));
     }
     const int incl = warp_incl_scan(run);
     if (lane == 31) scan[warp] = incl;
@@ -419,11 +420,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (between sinks and window, and all keys of an entry without new tokens):
     // the old weight, decayed
     if ((p.window > 0 || p.varlen) && !(prm.k.w_in == prm.k.w_out && prm.k.decay == 1.f)) {
+      const int* lens = reinterpret_cast<const int*>(smem + kLenOff);
       const int w_all = 2 * (int)gridDim.x, w_id = 2 * (int)blockIdx.x + (warp - 2);
       const int parts = max(1, w_all / prm.nb);
       for (int i = w_id / parts; i < prm.nb; i += w_all / parts) {
         if (w_id / parts >= w_all / parts) break;
-        const Entry e = load_entry(prm, i, false);
+        const Entry e = make_entry(prm, i, lens[i], false);
         const int n = (int)min((int64_t)e.n, prm.k.cols);
         int k0 = 0, k1 = n;
         if (entry_tiles(p, e) > 0) {
