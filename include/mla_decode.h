@@ -447,7 +447,8 @@ int mla_kv_amax(const void* latent, const void* rope, int64_t n_tokens, int in_d
  *   lse           device fp32 [B, q_len, H] or [total_q, H], as written by the
  *                 attention call
  *   weights_in    device fp32, row b at weights_in + b * in_stride; NULL stands
- *                 for zeros. Not read when decay is 0. May be weights_out
+ *                 for zeros. Not read when decay is 0. May be weights_out, with
+ *                 its stride; it must not overlap it in another way
  *   decay         finite, >= 0
  *   weights_out   device fp32, row b at weights_out + b * out_stride
  *   cols          columns of both, >= min(plan->max_seq_len,

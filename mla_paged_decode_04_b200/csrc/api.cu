@@ -59,6 +59,18 @@ bool device_addressable(const void* ptr, int dev) {
   return false;
 }
 
+// Whether two arrays of `rows` rows of fp32 (row r at p + r * ps, pc columns)
+// share an element: exact for equal strides (column slices of one buffer may
+// interleave), by their whole extents otherwise.
+bool rows_overlap(const float* p, int64_t ps, int64_t pc, const float* q, int64_t qs, int64_t qc, int64_t rows) {
+  const intptr_t a = reinterpret_cast<intptr_t>(p), b = reinterpret_cast<intptr_t>(q);
+  const intptr_t a_end = a + 4 * ((rows - 1) * ps + pc), b_end = b + 4 * ((rows - 1) * qs + qc);
+  if (a >= b_end || b >= a_end) return false;
+  if (ps != qs || rows == 1) return true;
+  const intptr_t m = (((b - a) % (4 * ps)) + 4 * ps) % (4 * ps);  // where q's columns begin in p's rows
+  return m < 4 * pc || m + 4 * qc > 4 * ps;
+}
+
 // The plan must be one the planner could have produced for its own fields.
 int check_plan(const mla_plan* p) {
   if (!p || p->magic != kPlanMagic) return MLA_ERR_PLAN_MISMATCH;
@@ -452,6 +464,11 @@ extern "C" int mla_key_weights(const mla_plan* plan, const void* q, int64_t tota
   if (cols < (p.max_seq_len < table_keys ? p.max_seq_len : table_keys) || out_stride < cols ||
       (weights_in && in_stride < cols))
     return MLA_ERR_INVALID_ARG;
+  if (decay == 0.f) weights_in = nullptr;  // not read
+  // in place is fine (a key's thread reads its old weight before it writes the new one); shifted in place is not
+  if (weights_in && !(weights_in == weights_out && in_stride == out_stride) &&
+      rows_overlap(weights_in, in_stride, cols, weights_out, out_stride, cols, p.batch))
+    return MLA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_failure(e);
   if ((total_q > 0 && (!device_addressable(q, dev) || !device_addressable(lse, dev))) ||
@@ -470,12 +487,12 @@ extern "C" int mla_key_weights(const mla_plan* plan, const void* q, int64_t tota
   k.a.max_pages_per_seq = max_pages_per_seq;
   k.a.seq_lens = seq_lens;
   k.a.score_scale_log2 =
-      (float)((double)softmax_scale * (fp8 ? (double)q_scale * kv_scale : 1.0) * (double)kLog2e);
+      (float)((double)softmax_scale * (fp8 ? (double)q_scale * kv_scale : 1.0) * 1.4426950408889634);
   k.a.status = device_status;
   k.a.cu_q = cu_seqlens_q;
   k.a.total_q = total_q;
   k.lse = lse;
-  k.w_in = decay != 0.f ? weights_in : nullptr;
+  k.w_in = weights_in;
   k.in_stride = in_stride;
   k.decay = decay;
   k.w_out = weights_out;
@@ -511,11 +528,8 @@ extern "C" int mla_cache_evict(const float* weights, int64_t weights_stride, int
   // A result on the pages it is gathered from, or new weights over the old,
   // would overwrite what is still to be read.
   if (kv_cache == out_cache && block_tables == out_block_tables) return MLA_ERR_INVALID_ARG;
-  if (out_weights) {
-    const float* w_end = weights + (int64_t)(batch - 1) * weights_stride + cols;
-    const float* o_end = out_weights + (int64_t)(batch - 1) * out_weights_stride + budget;
-    if (out_weights < w_end && weights < o_end) return MLA_ERR_INVALID_ARG;
-  }
+  if (out_weights && rows_overlap(weights, weights_stride, cols, out_weights, out_weights_stride, budget, batch))
+    return MLA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_failure(e);
   if (!device_addressable(weights, dev) || !device_addressable(seq_lens, dev) || !device_addressable(kv_cache, dev) ||

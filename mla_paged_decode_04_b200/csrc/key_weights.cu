@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
 #pragma unroll
           for (int i = 0; i < MLA_D_QK / 32; ++i)
             dot = fmaf(load_elem<DT>(a.q, row * MLA_D_QK + lane + 32 * i), kv[i], dot);
-          sum += exp2f(fmaf(warp_sum(dot), a.score_scale_log2, -lse * kLog2e));
+          sum += exp2f(fmaf(warp_sum(dot), a.score_scale_log2, (float)((double)lse * -1.4426950408889634)));
         }
       }
     }

@@ -467,7 +467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int last = -1;
         if (r < nr) {
           const float l = prm.k.lse[e.q0 * H + r0 + r];
-          x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys adds 0
+          // (rounded once: an error here weighs on every key of the row)
+          x = l == -INFINITY ? -INFINITY : (float)((double)l * -1.4426950408889634);  // a row without keys adds 0
           last = e.n - e.qlen + (r0 + r) / H;
         }
         lse_st[at + r] = x;

@@ -1,12 +1,14 @@
 """Windowed attention with sinks, received key weights and cache eviction on the GPU, against plain 64-bit forms.
 The bounds come from the roundings each path makes (long_context_ref.py)."""
 import math
+import types
 
 import pytest
 import torch
 
 import long_context_ref as ref
 import mla_paged_decode_04_b200 as mla
+from mla_paged_decode_04_b200 import _lib
 from mla_paged_decode_04_b200.inputs import make_inputs_custom, make_prefill_inputs
 
 pytestmark = pytest.mark.gpu
@@ -252,13 +254,109 @@ def test_key_weights_without_new_tokens_only_decay(cuda_device):
     assert torch.equal(got[0], w[0] * 0.5) and torch.equal(got[1, :30], w[1, :30] * 0.5) and (got[1, 30:] == 0).all()
 
 
+def test_key_weights_between_slices_of_one_buffer(cuda_device):
+    g = make_inputs_custom(3, 1, 32, "bf16", [300, 100, 7], seed=8, pool=1.5).to(cuda_device)
+    dec, _, lse = decode(g, 0, 0)
+    args = (g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse)
+    both = torch.rand(3, 600, device=cuda_device)
+    old = both[:, 300:].clone()
+    want = dec.key_weights(*args, both[:, :300].clone(), weights=old)
+    dec.key_weights(*args, both[:, :300], weights=both[:, 300:])
+    assert torch.equal(both[:, :300], want) and torch.equal(both[:, 300:], old)
+    with pytest.raises(mla.MlaError) as e:
+        dec.key_weights(*args, both[:, 1:301], weights=both[:, :300])
+    assert e.value.code == -1
+
+
+def test_key_weights_of_more_entries_than_one_launch_takes(cuda_device):
+    """1024 entries' tile counts fit a launch's shared memory; the rest go to further launches."""
+    lens = [(11 * i) % 90 for i in range(1500)]
+    g = make_inputs_custom(1500, 1, 3, "fp8", lens, seed=12, pool=1.1).to(cuda_device)
+    dec, _, lse = decode(g, 0, 0)
+    after = torch.full((1500, 90), -1.0, device=cuda_device)
+    dec.key_weights(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse, after, q_scale=g.q_scale,
+                    kv_scale=g.kv_scale)
+    assert dec.status() == 0
+    want, tol = ref.key_weights(g, lse.reshape(-1, 3), None, 1.0, 90)
+    past = torch.arange(90, device=cuda_device)[None] >= g.seq_lens[:, None]
+    assert (after[past] == -1.0).all()
+    ref.close(torch.where(past, 0.0, after), want, tol, "1500 entries")
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+def test_windowed_prefill_with_long_piece_lists(cuda_device, dtype):
+    """One token per unit (65 heads): the pairs' lists go past the pieces whose geometry is kept (32) and past those
+    in shared memory (64)."""
+    new = [400] * 12 + [3, 0]
+    g = make_prefill_inputs(new, [0, 5, 50, 64] * 3 + [700, 9], 65, dtype, seed=44, pool=1.2, device="cuda")
+    g = g.to(cuda_device)
+    pre, out, lse = prefill(g, 40, 3)
+    assert pre.status() == 0
+    check_attention(g, out, lse, 40, 3, "auto", dtype)
+
+
+def test_sinks_at_full_sequence_length(cuda_device):
+    """Pages far into a long sequence: 80,000 keys, of which a window and the sinks are read."""
+    g = make_inputs_custom(2, 4, 32, "fp8", [80001, 79000], seed=77, pool=1.0, ).to(cuda_device)
+    dec, out, lse = decode(g, 1500, 100)
+    assert dec.status() == 0
+    check_attention(g, out, lse, 1500, 100, "auto", "long")
+    after = torch.zeros(2, 80001, device=cuda_device)
+    dec.key_weights(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse, after, q_scale=g.q_scale,
+                    kv_scale=g.kv_scale)
+    want, tol = ref.key_weights(g, lse.reshape(-1, 32), None, 1.0, 80001, 1500, 100)
+    ref.close(after, want, tol, "long weights")
+
+
+def test_a_wait_that_runs_out_with_sinks(cuda_device):
+    """The FP8 pair kernel's failure-detection mode (its first tiles are never loaded, the waits for them end after
+    their limit) on a plan with sinks; the next call is clean."""
+    g = make_inputs_custom(2, 4, 32, "fp8", [3000, 1200], seed=62, pool=2.0).to(cuda_device)
+    dec, out, lse = decode(g, 500, 4)
+    faulty = type(dec.plan).from_buffer_copy(dec.plan)
+    faulty.fault_test = 1
+    mla.mla_decode(faulty, g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, out.clone(), lse.clone(),
+                   dec.workspace, g.q_scale, g.kv_scale)
+    torch.cuda.synchronize()
+    assert dec.status() & mla.MLA_DEV_TIMEOUT
+    again, lse2 = dec(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, g.q_scale, g.kv_scale)
+    assert dec.status() == 0 and torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "bf16"])
+def test_sinks_through_the_bounds_checking_build(cuda_device, dtype, monkeypatch):
+    monkeypatch.setattr(_lib, "_lib", _lib.load_library(_lib.CHECK_LIB_PATH))
+    assert mla.bounds_checked()
+    for lens, window, sinks in (([3000, 65, 1], 500, 4), ([1000, 391, 130], 70, 130)):
+        g = make_inputs_custom(3, 4, 32, dtype, lens, seed=63, pool=2.0).to(cuda_device)
+        dec, out, lse = decode(g, window, sinks)
+        assert dec.status() == 0
+        check_attention(g, out, lse, window, sinks, "auto", f"checking build {dtype}")
+    g = make_prefill_inputs([3, 50, 1, 64], [100, 0, 4000, 63], 32, dtype, seed=201).to(cuda_device)
+    pre, out, lse = prefill(g, 90, 65)
+    assert pre.status() == 0
+    check_attention(g, out, lse, 90, 65, "auto", f"checking build {dtype} prefill")
+
+
 def evict_inputs(lens, dtype, budget, seed, device):
-    g = make_inputs_custom(len(lens), 1, 1, dtype, lens, seed=seed, pool=1.5).to(device)
+    """A cache of random bytes (rows move as they are, whatever they hold), its tables, and the pages to go to."""
+    gen = torch.Generator(device=device).manual_seed(seed)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp8": torch.float8_e4m3fn}[dtype]
+    need = [(n + 63) // 64 for n in lens]
+    pool = int(1.5 * sum(need)) + 1
+    raw = torch.randint(0, 256, (pool, 64, 576 * dt.itemsize), generator=gen, device=device, dtype=torch.uint8)
+    perm = torch.randperm(pool, generator=gen, device=device).to(torch.int32)
+    tables = torch.full((len(lens), max(need + [1])), -1, dtype=torch.int32, device=device)
+    at = 0
+    for b, k in enumerate(need):
+        tables[b, :k] = perm[at:at + k]
+        at += k
+    g = types.SimpleNamespace(kv_cache=raw.view(dt), block_tables=tables,
+                              seq_lens=torch.tensor(lens, dtype=torch.int32, device=device))
     per = (budget + 63) // 64
     pages = len(lens) * per + 3
-    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(seed))[:len(lens) * per]
-    out_tables = perm.to(torch.int32).view(len(lens), per).to(device)
-    out_cache = torch.full((pages, 64, 576), 1.5, device=device).to(g.kv_cache.dtype)
+    out_tables = torch.randperm(pages, generator=gen, device=device)[:len(lens) * per].to(torch.int32).view(-1, per)
+    out_cache = torch.full((pages, 64, 576), 1.5, device=device).to(dt)
     return g, out_cache, out_tables
 
 
@@ -297,6 +395,9 @@ EVICTIONS = [
     ([4097, 33], 1, 0, 0),                # one key stays
     ([4097, 33], 1, 0, 1),
     ([40000, 17], 5000, 4, 64),
+    ([(13 * i) % 200 for i in range(230)], 70, 3, 9),        # one CTA an entry that moves its rows too
+    ([(131 * i) % 5000 for i in range(70)], 300, 3, 9),      # a cluster an entry that moves its rows too
+    ([400000], 600, 4, 100),                                  # a stretch longer than shared memory holds
 ]
 
 

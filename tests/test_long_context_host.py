@@ -69,7 +69,9 @@ def test_key_weights_refuses_bad_arguments_before_any_launch():
     inf, nan = float("inf"), float("nan")
     for kw in (dict(pages=0), dict(maxp=0), dict(scale=inf), dict(scale=nan), dict(decay=nan), dict(decay=inf),
                dict(decay=-0.5), dict(qs=0.0), dict(ks=nan), dict(cols=999), dict(out_stride=1023),
-               dict(in_stride=1023), dict(cols=2000)):
+               dict(in_stride=1023), dict(cols=2000),
+               dict(w_in=FAKE + 4), dict(w_in=FAKE + 4 * 1023), dict(w_in=FAKE, in_stride=1025),  # shifted in place
+               dict(w_in=FAKE + 4 * 500, in_stride=1500, out_stride=1500)):
         assert weights_call(p, **kw) == -1, kw
     assert weights_call(p, page_size=32) == -2
     assert weights_call(p, pages=(1 << 25) + 1) == -2
@@ -79,6 +81,14 @@ def test_key_weights_refuses_bad_arguments_before_any_launch():
     assert weights_call(r, cu=FAKE, total_q=19) == -1
     assert weights_call(r, cu=FAKE, total_q=-1) == -1
     assert weights_call(mla.mla_decode_plan(0, 4, 32, 1000, "fp8"), q=0, kv=0) == 0  # an empty batch
+
+
+def test_weights_may_lie_beside_each_other_in_one_buffer():
+    """Column slices of one buffer do not overlap; the call gets past that check (and ends at the host pointers)."""
+    p = mla.mla_decode_plan(2, 4, 32, 1000, "fp8")
+    code = weights_call(p, w_in=FAKE + 4 * 1024, in_stride=2048, out_stride=2048)
+    assert code in (-1, -4, -5) and code == weights_call(p)
+    assert weights_call(p, w_in=FAKE + 4 * 1023, in_stride=2048, out_stride=2048) == -1
 
 
 def evict_call(**kw):
