@@ -60,6 +60,12 @@ constexpr int kMaxEntries = 1024;  // entries of one launch: their tiles and len
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlots = 9;     // ring slots a tile is cut into
 constexpr uint32_t kChunkBytes = 128 * 128;
+// 16-bit scores of few rows (N <= 64) go to four accumulators of a quarter of
+// the dims each, added in fp32 afterwards. The tensor cores cut each partial sum
+// toward zero, which leaves up to 1.4e-6 on a key's weight where no other rows
+// average it out (one head, FP16); of four smaller sums 5e-7 is left.
+constexpr int kParts = 4;
+constexpr int kPartCols = 64;
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kStartOff = 0;                                   // int [kMaxEntries + 1]: first tile of an entry
@@ -89,6 +95,7 @@ struct KeyWeightParams {
   KeyWeightArgs k;
   int b0, nb;        // this launch's entries
   int n_cols;        // N: rows per group (a multiple of 32)
+  int parts;         // accumulators the dims are spread over (1 or kParts)
   int stages;
   uint32_t idesc;
 };
@@ -283,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const uint32_t tmem = *tmem_slot;
+  const bool spread = E == 2 && kForm == kRowsStay && prm.parts > 1;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -386,14 +394,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t more = C::rope(c) ? rope_bits : 0ull;
             const uint64_t dr = res_desc + (uint64_t)(c * (res_slot >> 4)) + more;
             const uint64_t ds = slot_desc + (uint64_t)((c - C::first(s)) * (kChunkBytes >> 4)) + more;
+            // (the part of chunk c, and whether it begins there)
+            const int part = c * kParts / C::kChunks;
+            const bool begins = c == 0 || part != (c - 1) * kParts / C::kChunks;
+            const uint32_t dp = d + (spread ? (uint32_t)(kPartCols * part) : 0u);
+            const uint32_t first = spread ? !begins : c > 0;
             const uint64_t dk = kForm == kKeysStay ? dr : ds;
             const uint64_t dq = kForm == kRowsStay ? dr : ds + (C::kRowsAt >> 4);
 #pragma unroll
             for (int kk = 0; kk < (C::rope(c) ? 2 : 4); ++kk) {  // 32 bytes of the dims per MMA
               if constexpr (E == 2)
-                mma_f16_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+                mma_f16_ss_pair_e(dp, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, kk ? 1u : first);
               else
-                mma_f8_ss_pair_e(d, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, (c | kk) ? 1u : 0u);
+                mma_f8_ss_pair_e(dp, dk + (uint64_t)(2 * kk), dq + (uint64_t)(2 * kk), prm.idesc, kk ? 1u : first);
             }
           }
           mma_commit_pair_mc_e(bar(B_EMPTY + st), 3);
@@ -494,6 +507,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t sv[32];
         tmem_ld32(tmem + tl + 256u * buf + 32u * cb, sv);
         tmem_wait_ld();
+        if (spread) {
+#pragma unroll 1
+          for (int part = 1; part < kParts; ++part) {
+            uint32_t more[32];
+            tmem_ld32(tmem + tl + 256u * buf + (uint32_t)(kPartCols * part) + 32u * cb, more);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = __float_as_uint(__uint_as_float(sv[i]) + __uint_as_float(more[i]));
+          }
+        }
         const float* lr = lse_st + at + 32 * cb;
         if (open && 32 * cb + 32 <= nr) {
 #pragma unroll
@@ -686,6 +709,7 @@ cudaError_t launch_key_weights_tc(const KeyWeightArgs& k, cudaStream_t stream) {
   KeyWeightParams prm;
   prm.k = k;
   prm.n_cols = N;
+  prm.parts = E == 2 && N <= kPartCols ? kParts : 1;
   const uint32_t fmt = p.dtype == MLA_BF16 ? 1u : 0u;  // BF16 = 1, FP16 = 0; E4M3 = 0 in its own kind
   prm.idesc = instr_desc(fmt, fmt, 0, 256, (uint32_t)N);
   // without a query token no tile is ever loaded; the maps still need an array
