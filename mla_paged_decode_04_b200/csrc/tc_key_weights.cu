@@ -27,8 +27,7 @@
 //   * kBothStream (16-bit, more than 128 rows): either resident part would take
 //     147 KB and leave a ring of 64 KB, 2048 cycles of MMAs. Without one the ring
 //     holds six slots of both operands' chunks, 3072 cycles; K is read again per
-//     group, from L2. (Ragged steps of 16 to 32 tokens x 64 heads over up to
-//     32,768 FP16 keys: @@OBS@@.)
+//     group, from L2 (the FP16 case below: 158 us with keys resident, 143 without).
 // With several row groups the sum goes on in registers from group to group,
 // and pairs take tiles a grid apart, whose numbers of groups (causal mask,
 // window) are alike. A resident operand is replaced slot by slot behind the
@@ -36,8 +35,17 @@
 //
 // Roles (384 threads per CTA): warp 0 loads, warp 1 of the leader issues the
 // MMAs, warps 2 and 3 write the keys that no row sees (their old weight,
-// decayed), warps 4-11 are two groups that take alternate score buffers: ex2
-// of the score minus the row's log-sum-exp (one FMA), summed over the rows.
+// decayed), warps 4-11 sum: ex2 of the score minus the row's log-sum-exp (one
+// FMA), over the rows. Up to 128 rows the two groups of four warps take alternate
+// score buffers; above, a buffer's 256 columns take a group as long as its MMAs
+// and more, so the two share every buffer (alternate 32 columns) and hand it back
+// in half the time (16..32 last tokens x 64 heads over 4 x up to 32,768 FP16
+// keys: 127 -> 118 us; 16 x 4 tokens x 64 heads over 81,920 FP8 keys: 207 -> 194 us).
+//
+// Measured: 16 x 4 tokens x 32 heads over 81,920 FP8 keys 132 us in replayed
+// graphs (5.8 TB/s, 0.89 of the copy bandwidth; 158 us where the power limit
+// holds the clock down), 4 x 4 x 32 over 8192 BF16 keys 16 us (two tiles a pair,
+// 5.9 us of HBM time).
 // Every wait is bounded as in the attention kernels. No TMA load uses
 // multicast.
 #include <cuda.h>
@@ -233,6 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0 = leader
   const int N = prm.n_cols, NB = N / 2, NS = prm.stages;
+  // whether the two sum groups share every tile (alternate columns)
+  const bool halves = kGroups || N > 128;
   // rows of a chunk, both operands' CTA halves: what stays, what a slot takes
   const int res_rows = kForm == kKeysStay ? kHalf : NB;
   const int ring_rows = kForm == kRowsStay ? kHalf : kForm == kKeysStay ? NB : kHalf + NB;
@@ -242,8 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x < kNumBars) {
     const int i = threadIdx.x;
-    // S_EMPTY: a sum group's warps in both CTAs; from LSE on a group's warps
-    mbar_init(bar(i), (i >= B_S_EMPTY && i < B_S_EMPTY + 2) ? 8u : i >= B_LSE ? 4u : 1u);
+    // S_EMPTY: the sum warps of a tile in both CTAs; from LSE on a group's warps
+    mbar_init(bar(i), (i >= B_S_EMPTY && i < B_S_EMPTY + 2) ? (halves ? 16u : 8u) : i >= B_LSE ? 4u : 1u);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) *abort_flag = issued[0] = issued[1] = 0;
@@ -469,41 +479,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     Walk w(prm, smem, kGroups);
 
-    // the constants of rows [r0, r0 + nr) of the entry: -lse * log2(e), and the
-    // newest key each row sees (-1 past the group)
-    auto stage = [&](const Entry& e, int r0, int nr) {
+    // This thread's rows of a row group [r0, r0 + nr): two of all 256 columns, or
+    // one of the half that its sum group takes (columns 32 cb .. 32 cb + 31 with
+    // cb of the group's parity).
+    auto own_row = [&](int u) -> int { return halves ? 64 * (tid >> 5) + 32 * grp + lane : tid + 128 * u; };
+    struct RowLse {
+      float l[2];
+    };
+    auto load_lse = [&](const Entry& e, int r0, int nr) -> RowLse {
+      RowLse x;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = own_row(u);
+        x.l[u] = (u == 0 || !halves) && r < nr ? prm.k.lse[e.q0 * H + r0 + r] : -INFINITY;
+      }
+      return x;
+    };
+    // their constants into shared memory: -lse * log2(e), and where a batch of 32
+    // columns has masked pairs or ends the group the newest key each row sees (-1
+    // past the group)
+    auto stage = [&](const Entry& e, int r0, int nr, const RowLse& x, bool masks) {
       const int at = (staged & 1) * 256;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int r = tid + 128 * u;
-        float x = -INFINITY;
-        int last = -1;
-        if (r < nr) {
-          const float l = prm.k.lse[e.q0 * H + r0 + r];
-          // (rounded once: an error here weighs on every key of the row)
-          x = l == -INFINITY ? -INFINITY : (float)((double)l * -1.4426950408889634);  // a row without keys adds 0
-          last = e.n - e.qlen + (r0 + r) / H;
-        }
-        lse_st[at + r] = x;
-        last_st[at + r] = last;
+        if (u == 1 && halves) break;
+        const int r = own_row(u);
+        const float l = x.l[u];
+        // (rounded once: an error here weighs on every key of the row; a row without keys adds 0)
+        lse_st[at + r] = l == -INFINITY ? -INFINITY : (float)((double)l * -1.4426950408889634);
+        if (masks) last_st[at + r] = r < nr ? e.n - e.qlen + (r0 + r) / H : -1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_LSE + grp));
       ok = warp_wait_cta(bar(B_LSE + grp), staged & 1, abort_flag, a.status);
       ++staged;
     };
+    // whether every row of the group sees every key of this CTA's half tile
+    auto open_tile = [&](const Entry& e, int r0, int nr, int key0) -> bool {
+      const int last_a = e.n - e.qlen + r0 / H, last_b = e.n - e.qlen + (r0 + nr - 1) / H;
+      return key0 + kHalf - 1 <= last_a && (key0 > last_b - W || key0 + kHalf <= sinks);
+    };
     // sum over the group's rows of item t's scores (buffer t & 1)
-    auto sum_rows = [&](const Entry& e, int r0, int nr, int key0, int t) -> float {
+    auto sum_rows = [&](int nr, int key0, int t, bool open) -> float {
       const int at = ((staged - 1) & 1) * 256;
       const int buf = t & 1, key = key0 + kl;
       if (!(ok = warp_wait_cta(bar(B_S_FULL + buf), (t >> 1) & 1, abort_flag, a.status))) return 0.f;
       tc_fence_after();
-      // every row of the group sees every key of this CTA's half tile
-      const int last_a = e.n - e.qlen + r0 / H, last_b = e.n - e.qlen + (r0 + nr - 1) / H;
-      const bool open = key0 + kHalf - 1 <= last_a && (key0 > last_b - W || key0 + kHalf <= sinks);
       uint64_t s2[2] = {0ull, 0ull};
       float s1 = 0.f;
-      for (int cb = 0; 32 * cb < nr; ++cb) {
+      for (int cb = halves ? grp : 0; 32 * cb < nr; cb += halves ? 2 : 1) {
         uint32_t sv[32];
         tmem_ld32(tmem + tl + 256u * buf + 32u * cb, sv);
         tmem_wait_ld();
@@ -575,29 +599,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto tile_key = [&]() -> int { return kTile * w.tile(p) + kHalf * (int)rank; };
 
-    if constexpr (kGroups) {
+    if (halves) {
       Ahead next{0.f, 0};
-      if (w.more()) {
-        w.seek(prm);
+      RowLse next_l{};
+      int ng0 = 0, ng1 = 1;
+      bool next_other = true;
+      auto look_ahead = [&]() {  // the next tile's constants, on their way while this one is summed
+        next_other = w.seek(prm);
         next = ahead(w.e, tile_key());
-      }
+        if (kGroups) tile_groups(prm, w.e, kTile * w.tile(p), ng0, ng1);
+        if (kGroups || next_other) next_l = load_lse(w.e, ng0 * N, min(N, w.e.rows - ng0 * N));
+      };
+      if (w.more()) look_ahead();
       while (ok && w.more()) {
         const Entry e = w.e;
-        const int key0 = tile_key(), key = key0 + kl;
+        const int key0 = tile_key(), key = key0 + kl, g0 = ng0, g1 = ng1;
         const Ahead cur = next;
-        int g0, g1;
-        tile_groups(prm, e, kTile * w.tile(p), g0, g1);
+        const bool other = next_other;
+        RowLse cur_l = next_l;
         w.idx += w.step;
-        if (w.more()) {
-          w.seek(prm);
-          next = ahead(w.e, tile_key());
-        }
+        if (w.more()) look_ahead();
         float sum = 0.f;
         for (int g = g0; ok && g < g1; ++g, ++jt) {
-          if ((jt & 1) != grp) continue;
           const int nr = min(N, e.rows - g * N);
-          stage(e, g * N, nr);
-          if (ok) sum += sum_rows(e, g * N, nr, key0, jt);
+          const bool open = open_tile(e, g * N, nr, key0);
+          // (one group: its rows stay staged, with their newest keys, for the entry's next tiles)
+          if (kGroups || other) stage(e, g * N, nr, cur_l, !kGroups || !open || (nr & 31));
+          if (g + 1 < g1) cur_l = load_lse(e, (g + 1) * N, min(N, e.rows - (g + 1) * N));
+          if (ok) sum += sum_rows(nr, key0, jt, open);
         }
         if (!ok) break;
         // group 1's part through shared memory, then the sum in a fixed order
@@ -634,14 +663,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int key0 = tile_key(), key = key0 + kl, t = jt;
         const Ahead cur = next;
         if (staged_for != e.b) {
-          stage(e, 0, e.rows);
+          stage(e, 0, e.rows, load_lse(e, 0, e.rows), true);
           staged_for = e.b;
           if (!ok) break;
         }
         ++w.idx, ++jt;
         to_own();
         if (w.more()) next = ahead(w.e, tile_key());
-        const float sum = sum_rows(e, 0, e.rows, key0, t);
+        const float sum = sum_rows(e.rows, key0, t, open_tile(e, 0, e.rows, key0));
         if (!ok) break;
         write(e, key, cur.old, check_page(cur.entry) ? sum : 0.f);
       }
