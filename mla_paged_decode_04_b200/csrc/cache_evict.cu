@@ -22,10 +22,14 @@
 // Moving. HBM-bound: 2 * 576 (FP8) or 2 * 1152 bytes per row that stays. A warp
 // takes 288 16-byte chunks at a time (8 FP8 or 4 16-bit rows): the lanes look up
 // the rows' places together, then each has nine loads in flight before its
-// first store. With CTAs enough for three of every four places each cluster moves its own
-// entry's rows as soon as it has chosen them (one launch, and entries that are
-// done early fill the memory system while others select); with fewer a second
-// kernel, a programmatic dependent, spreads the rows over all SMs.
+// first store. Where the clusters fill three of four places (two CTAs an SM),
+// each moves its own entry's rows as soon as it has chosen them: one launch, and
+// entries that are done early keep HBM busy while others select. With fewer a
+// second kernel, a programmatic dependent, spreads the rows over all SMs.
+//
+// Measured (replayed graphs): 16 x 81,920 FP8 weights to 8192 keys 50 us, of
+// which the selection 22 and the moving 28 (5.4 TB/s); 64 x 1000..16,384 BF16 to
+// 2000 keys 64 us (4.5 TB/s in all); one entry of 1100 keys to 1024 8 us.
 #include "device_common.cuh"
 #include "sm100_ptx.cuh"
 

@@ -26,7 +26,7 @@
 //     comes from HBM once; a 16 KB chunk from L2 feeds 256 x 256 x 128 products.
 //   * kBothStream (16-bit, more than 128 rows): either resident part would take
 //     147 KB and leave a ring of 64 KB, 2048 cycles of MMAs. Without one the ring
-//     holds six slots of both operands' chunks, 3072 cycles; K is read again per
+//     holds six slots of both operands' chunks, half as much again; K is read per
 //     group, from L2 (the FP16 case below: 158 us with keys resident, 143 without).
 // With several row groups the sum goes on in registers from group to group,
 // and pairs take tiles a grid apart, whose numbers of groups (causal mask,
