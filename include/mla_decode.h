@@ -506,8 +506,9 @@ int mla_key_weights(const mla_plan* plan, const void* q, int64_t total_q, const 
  *
  * Nothing is allocated or synchronised; capturable in a CUDA graph. Errors:
  * MLA_ERR_INVALID_ARG (budget < 1, sinks + recent > budget, overlaps, null or
- * misaligned pointers), MLA_ERR_UNSUPPORTED_SHAPE, MLA_ERR_ARCH, MLA_ERR_CUDA.
- * batch = 0 is a no-op.
+ * misaligned pointers), MLA_ERR_UNSUPPORTED_SHAPE (page size; a budget, or columns
+ * and table both, of more than 2^30 keys), MLA_ERR_ARCH, MLA_ERR_CUDA. batch = 0
+ * is a no-op.
  */
 int mla_cache_evict(const float* weights, int64_t weights_stride, int64_t cols, const int32_t* seq_lens, int batch,
                     int budget, int sinks, int recent, const void* kv_cache, int64_t num_pages, int page_size,

@@ -134,6 +134,11 @@ int check_plan(const mla_plan* p) {
 
 namespace {
 
+// A plan's window for the kernels: past the longest sequence (2^30 keys) it no
+// longer matters, and there a key's place less the window fits an int even for
+// the rows before an entry's first key.
+int32_t device_window(const mla_plan& p) { return p.window < (1 << 30) ? p.window : 1 << 30; }
+
 // Validate the arguments and fill the launch description. Returns MLA_OK or
 // an error code; nothing is enqueued here.
 // cu_q: null for decode (every entry has the plan's q_len tokens); for a
@@ -177,6 +182,7 @@ int prepare(const mla_plan* plan, const void* q, const void* kv_cache, int64_t n
 
   *a = DecodeArgs{};
   a->plan = p;
+  a->plan.window = device_window(p);
   a->q = q;
   a->kv_cache = kv_cache;
   a->num_pages = num_pages;
@@ -480,6 +486,7 @@ extern "C" int mla_key_weights(const mla_plan* plan, const void* q, int64_t tota
   if (int rc = check_device_arch(); rc != MLA_OK) return rc;
   KeyWeightArgs k{};
   k.a.plan = p;
+  k.a.plan.window = device_window(p);
   k.a.q = q;
   k.a.kv_cache = kv_cache;
   k.a.num_pages = num_pages;
@@ -523,6 +530,9 @@ extern "C" int mla_cache_evict(const float* weights, int64_t weights_stride, int
   if (num_pages < 1 || out_num_pages < 1 || max_pages_per_seq < 1 || cols < 1 || weights_stride < cols ||
       (out_weights && out_weights_stride < budget) || (int64_t)out_max_pages_per_seq * MLA_PAGE_SIZE < budget)
     return MLA_ERR_INVALID_ARG;
+  const int64_t table_keys = (int64_t)max_pages_per_seq * MLA_PAGE_SIZE;
+  if ((cols < table_keys ? cols : table_keys) > (int64_t(1) << 30) || budget > (1 << 30))
+    return MLA_ERR_UNSUPPORTED_SHAPE;  // places of keys are ints
   if (num_pages > (int64_t(1) << 40) / MLA_PAGE_SIZE || out_num_pages > (int64_t(1) << 40) / MLA_PAGE_SIZE)
     return MLA_ERR_UNSUPPORTED_SHAPE;
   // A result on the pages it is gathered from, or new weights over the old,

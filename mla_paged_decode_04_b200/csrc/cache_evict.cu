@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) cache_evict_move_kernel(const EvictArgs e
   ptx::grid_dep_wait();
   for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < total; it += warps) {
     const int b = (int)(it / steps), step = (int)(it - (int64_t)b * steps);
-    const int len = e.out_seq_lens[b];
+    const int len = __ldcg(e.out_seq_lens + b);  // (may be seq_lens, which L1 may hold as it was)
     if (step < move_steps<kRowBytes>(len)) move_step<kRowBytes>(e, b, step, len);
   }
 }

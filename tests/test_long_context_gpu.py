@@ -87,6 +87,21 @@ def test_sinks_without_effect_leave_every_bit(cuda_device, dtype):
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype", ["fp16", "fp8"])
+def test_the_longest_window_with_fewer_keys_than_tokens(cuda_device, dtype, kernel):
+    """A window of 2^31 - 1 stands for none, also where a row's last place is far below zero."""
+    g = make_inputs_custom(4, 9, 20, dtype, [2, 0, 70, 9], seed=15, pool=1.5).to(cuda_device)
+    for sinks in (0, 3):
+        dec, out, lse = decode(g, (1 << 31) - 1, sinks, kernel)
+        check_attention(g, out, lse, 0, 0, kernel, f"{sinks} sinks")
+        got = dec.key_weights(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse,
+                              torch.zeros(4, 70, device=cuda_device), q_scale=g.q_scale, kv_scale=g.kv_scale)
+        assert dec.status() == 0
+        want, tol = ref.key_weights(g, lse.reshape(-1, 20), None, 1.0, 70)
+        ref.close(got, want, tol, f"{sinks} sinks, weights")
+
+
 def poisoned(g, window, sinks):
     """The same step with NaN in every place no row sees: the rest of the last page, the pages between sinks and
     window, whose table entries are -1, and page 0 of the pool where no entry owns it."""

@@ -117,6 +117,10 @@ def test_cache_evict_refuses_bad_arguments_before_any_launch():
                dict(out_w=FAKE + 400), dict(out_w=9 * FAKE, out_w_stride=127)):
         assert evict_call(**kw) == -1, kw
     assert evict_call(page_size=16) == -2
+    # places of keys are ints: no more than 2^30 of them, where columns and table both allow more
+    many = (1 << 30) // 64
+    assert evict_call(cols=(1 << 30) + 1, w_stride=(1 << 30) + 1, maxp=many + 1) == -2
+    assert evict_call(budget=(1 << 30) + 1, out_maxp=many + 1) == -2
     assert evict_call(batch=0) == 0
 
 
