@@ -23,6 +23,8 @@
 // and units.
 #pragma once
 
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -77,6 +79,31 @@ __device__ __forceinline__ UnitGeom load_geo(const PieceGeo* g) {
   return ug;
 }
 constexpr int kMinPairWeight = 4;  // pairs get at least this much weight (>= the heaviest tile)
+
+// With sinks a unit's span, and so its pieces, is often short. What cutting its
+// weight w into n pieces costs is about a w / n for the tiles and b n for the
+// merge, least at n = sqrt(a / b w); a / b is about 4 (one unit of 284 tile
+// weights, FP16: 33.7 us in 71 pieces, 28.1 in 47, 24.8 in 35, 30.5 in 12; one
+// of 123, FP8: 24.1 us in 30, 19.8 in 20, 22.1 in 10), and no pair takes fewer
+// than two tiles (a unit of three FP8 tiles: 17.3 us against 18.6).
+__host__ __device__ __forceinline__ int most_pairs_with_sinks(const mla_plan& p, int64_t weight, int more) {
+  const int64_t by_two = weight / (p.dtype == MLA_FP8_E4M3 ? 6 : 4);
+  const int64_t by_merge = (int64_t)sqrtf(4.f * (float)weight * (float)(p.batch * p.q_groups)) + more;
+  return (int)(by_two < by_merge ? by_two : by_merge);
+}
+// Pairs to launch: no more than build_schedule can hand work, where a window
+// with sinks bounds a unit's tiles (idle pairs cost a call of one short unit
+// 0.9 us of 18.5).
+inline int launch_pairs(const mla_plan& p, int keys) {
+  if (!plan_has_sinks(p)) return p.split_kv;
+  const int per = keys / kTileKeys, units = p.batch * p.q_groups;
+  // (window + fold - 1 keys anywhere in their first page, and the sinks)
+  const int64_t pages = std::min(((int64_t)p.window + p.fold + 125) / kTileKeys + ((int64_t)p.sinks + 63) / kTileKeys,
+                                 ((int64_t)p.max_seq_len + kTileKeys - 1) / kTileKeys);
+  const int64_t w = (int64_t)units * (kPieceLeadWeight + (p.dtype == MLA_FP8_E4M3 ? 3 : 2) * ((pages + per - 1) / per));
+  // (one more: the device may round the square root the other way)
+  return std::max(1, std::min(p.split_kv, most_pairs_with_sinks(p, w, 1)));
+}
 
 // Unit at schedule slot s, and the slot of unit u (u = entry * G + group).
 __host__ __device__ __forceinline__ bool sched_group_major(const mla_plan& p) {
@@ -233,7 +260,7 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
     if (w < warp) excl += x;
     W += x;
   }
-  const int np = max(1, min(p.split_kv, W / kMinPairWeight));
+  const int np = max(1, min(p.split_kv, kSinks ? most_pairs_with_sinks(p, W, 0) : W / kMinPairWeight));
   const int64_t lo = pair < np ? balanced_lo(pair, W, np) : W;
   const int64_t hi = pair < np ? balanced_lo(pair + 1, W, np) : W;
   if (writer) {

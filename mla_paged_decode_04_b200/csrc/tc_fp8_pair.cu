@@ -1063,7 +1063,7 @@ cudaError_t launch_tc_fp8_pair_partial(const DecodeArgs& a, cudaStream_t stream)
   // a programmatic dependent of the previous kernel in the stream (the
   // workspace clear): it waits for it before touching global memory
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * p.split_kv));
+  cfg.gridDim = dim3((unsigned)(2 * launch_pairs(p, kPairTileKeys)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.stream = stream;
