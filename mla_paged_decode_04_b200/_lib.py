@@ -10,6 +10,7 @@ kernels set MLA_DEV_BOUNDS instead of accessing memory outside a buffer).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -317,6 +318,15 @@ def _stream_of(t, stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
+def _allocating_on(t, stream):
+    """Context in which torch allocates and fills for work that is launched on `stream`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, t.device) if stream else torch.cuda.default_stream(t.device)
+    return torch.cuda.stream(stream)
+
+
 def kv_pack(latent, rope, slot_mapping, kv_cache, kv_scale=1.0, device_status=None, stream=None) -> None:
     """Write tokens into the paged cache, fused with FP8 quantisation when kv_cache is FP8.
 
@@ -432,16 +442,17 @@ def cache_evict(weights, seq_lens, kv_cache, block_tables, out_cache, out_block_
         raise ValueError("weights and the block tables must have one row per batch entry")
     if budget < 1:
         raise MlaError(MLA_ERR_INVALID_ARG, "mla_cache_evict")
-    if out_seq_lens is None:
-        out_seq_lens = torch.empty(B, dtype=torch.int32, device=seq_lens.device)
-    elif out_seq_lens.dtype is not torch.int32 or out_seq_lens.numel() != B:
+    with _allocating_on(seq_lens, stream):
+        if out_seq_lens is None:
+            out_seq_lens = torch.empty(B, dtype=torch.int32, device=seq_lens.device)
+        if kept is None:
+            kept = torch.empty((B, budget), dtype=torch.int32, device=seq_lens.device)
+        if out_weights is None:
+            out_weights = torch.zeros((B, budget), dtype=torch.float32, device=seq_lens.device)
+    if out_seq_lens.dtype is not torch.int32 or out_seq_lens.numel() != B:
         raise ValueError("out_seq_lens must be int32 [batch]")
-    if kept is None:
-        kept = torch.empty((B, budget), dtype=torch.int32, device=seq_lens.device)
-    elif kept.dtype is not torch.int32 or kept.dim() != 2 or kept.size(0) != B or kept.size(1) != budget:
+    if kept.dtype is not torch.int32 or kept.dim() != 2 or kept.size(0) != B or kept.size(1) != budget:
         raise ValueError("kept must be int32 [batch, budget]")
-    if out_weights is None:
-        out_weights = torch.zeros((B, budget), dtype=torch.float32, device=seq_lens.device)
     out_stride = _weight_rows("out_weights", out_weights, index)
     if out_weights.size(0) != B or out_weights.size(1) < budget:
         raise ValueError("out_weights must be float32 [batch, >= budget]")

@@ -480,6 +480,22 @@ def test_evict_within_one_pool_strided_weights_and_lengths_in_place(cuda_device)
     assert torch.equal(g.kv_cache[keep], before[keep])
 
 
+def test_evict_on_a_stream_of_its_own_fills_what_it_allocates_there(cuda_device):
+    """The current stream is busy: nothing it does later may touch the results of another stream."""
+    lens, budget = [900, 77], 128
+    g, out_cache, out_tables = evict_inputs(lens, "bf16", budget, 31, cuda_device)
+    w = 0.5 + torch.rand(2, 900, device=cuda_device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        got = mla.cache_evict(w, g.seq_lens, g.kv_cache, g.block_tables, out_cache, out_tables, budget, 4, 16,
+                              stream=stream)
+        torch.cuda.synchronize()
+        check_evicted(g, w, budget, 4, 16, out_cache, out_tables, got)
+        assert (got[2][0] >= 0.5).all()
+
+
 def test_evict_reports_bad_pages_and_lengths(cuda_device):
     g, out_cache, out_tables = evict_inputs([300, 200, 100], "fp8", 128, 5, cuda_device)
     tables, to = g.block_tables.clone(), out_tables.clone()
