@@ -13,7 +13,7 @@
 //
 // The weights are read from HBM once (4 bytes a key, little next to the rows
 // that move), so what bounds the selection is the latency of its passes. One
-// cluster of up to 8 CTAs per entry, each with its stretch of the weights in
+// CTA per entry or a cluster of up to 8, each with its stretch of the weights in
 // shared memory. After a pass CTA r sums its share of the bins over all
 // histograms through distributed shared memory; every CTA then knows the shares'
 // totals, reads the one share that holds the digit and finds it itself: two
@@ -404,11 +404,15 @@ cudaError_t launch_select(const EvictArgs& e, cudaLaunchConfig_t& cfg, int ctas,
 
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t stream) {
   // CTAs per entry: as many as the SMs hold at two each, with at least 1024
-  // candidates for each
+  // candidates for each; one for tables of few keys, since a cluster's launch and
+  // barriers cost 4 to 5 us whatever its entry (16 entries of 2500 keys: 12.7 us
+  // with one, 16.8 with clusters; of 9000 15.3 and 19.5; of 20,000 20.5 and 19.8; 64 of
+  // 9000 68.2 and 65.8)
   const int64_t longest = e.cols < (int64_t)e.max_pages_per_seq * kTileKeys ? e.cols
                                                                             : (int64_t)e.max_pages_per_seq * kTileKeys;
   int ctas = 1;
-  while (ctas < kMaxCluster && (int64_t)e.batch * ctas * 2 <= 2 * kNumSMs && longest >= 2048 * ctas) ctas *= 2;
+  constexpr int64_t kClusterKeys = 10240;
+  while (longest >= kClusterKeys && ctas < kMaxCluster && (int64_t)e.batch * ctas * 2 <= 2 * kNumSMs && longest >= 2048 * ctas) ctas *= 2;
   const int64_t stretch = (longest + ctas - 1) / ctas;
   const int held = stretch <= kMaxHeld ? (int)stretch : 0;
   // (64 entries, 256 CTAs: 64.5 us against 71.3 in two kernels; 16 entries, 128

@@ -411,7 +411,11 @@ EVICTIONS = [
     ([4097, 33], 1, 0, 1),
     ([40000, 17], 5000, 4, 64),
     ([(13 * i) % 200 for i in range(230)], 70, 3, 9),        # one CTA an entry that moves its rows too
-    ([(131 * i) % 5000 for i in range(70)], 300, 3, 9),      # a cluster an entry that moves its rows too
+    ([(131 * i) % 5000 for i in range(70)], 300, 3, 9),
+    ([(331 * i) % 11000 for i in range(70)], 300, 3, 9),     # a cluster of four an entry that moves its rows too
+    ([(331 * i) % 11000 for i in range(110)], 70, 3, 9),     # a cluster of two an entry
+    ([10300, 9, 10240], 5000, 0, 1),                         # a cluster of eight
+    ([10239] * 2, 5000, 0, 1),                               # the longest that one CTA takes
     ([400000], 600, 4, 100),                                  # a stretch longer than shared memory holds
 ]
 
