@@ -93,7 +93,8 @@ __host__ __device__ __forceinline__ int most_pairs_with_sinks(const mla_plan& p,
 }
 // Pairs to launch: no more than build_schedule can hand work, where a window
 // with sinks bounds a unit's tiles (idle pairs cost a call of one short unit
-// 0.9 us of 18.5).
+// 0.9 us of 18.5). A length above the plan's is not clamped to it, only to the
+// block table: build_schedule deals its tiles to the launched pairs too.
 inline int launch_pairs(const mla_plan& p, int keys) {
   if (!plan_has_sinks(p)) return p.split_kv;
   const int per = keys / kTileKeys, units = p.batch * p.q_groups;
@@ -260,7 +261,9 @@ __device__ void build_schedule(const DecodeArgs& a, int pair, uint32_t rank, uin
     if (w < warp) excl += x;
     W += x;
   }
-  const int np = max(1, min(p.split_kv, kSinks ? most_pairs_with_sinks(p, W, 0) : W / kMinPairWeight));
+  // (with sinks the grid may hold fewer pairs than the plan, see launch_pairs)
+  const int np = max(1, kSinks ? min((int)(gridDim.x >> 1), most_pairs_with_sinks(p, W, 0))
+                               : min(p.split_kv, W / kMinPairWeight));
   const int64_t lo = pair < np ? balanced_lo(pair, W, np) : W;
   const int64_t hi = pair < np ? balanced_lo(pair + 1, W, np) : W;
   if (writer) {
