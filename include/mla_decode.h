@@ -435,7 +435,8 @@ int mla_kv_amax(const void* latent, const void* rope, int64_t n_tokens, int in_d
  * for every key j < seq_lens[b]; columns from seq_lens[b] on are left as they
  * were. Call it after mla_decode (or mla_prefill) with that call's plan, q,
  * cache, tables and lse: causal mask, window and sinks are the plan's. A row
- * whose lse is -inf (no visible key) adds nothing.
+ * whose lse is -inf (no visible key, or set so to leave a padding row out) adds
+ * nothing, whatever its q holds.
  *
  *   plan          a decode plan, or with cu_seqlens_q a prefill plan. Kernel
  *                 MLA_KERNEL_SIMT takes the plain CUDA-core form; every other

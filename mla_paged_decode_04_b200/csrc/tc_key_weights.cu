@@ -50,6 +50,8 @@
 // multicast.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "pair_schedule.cuh"
 #include "sm100_ptx.cuh"
@@ -497,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // their constants into shared memory: -lse * log2(e), and where a batch of 32
     // columns has masked pairs or ends the group the newest key each row sees (-1
-    // past the group)
+    // past the group, and for a row whose lse is -inf)
     auto stage = [&](const Entry& e, int r0, int nr, const RowLse& x, bool masks) {
       const int at = (staged & 1) * 256;
 #pragma unroll
@@ -507,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float l = x.l[u];
         // (rounded once: an error here weighs on every key of the row; a row without keys adds 0)
         lse_st[at + r] = l == -INFINITY ? -INFINITY : (float)((double)l * -1.4426950408889634);
-        if (masks) last_st[at + r] = r < nr ? e.n - e.qlen + (r0 + r) / H : -1;
+        if (masks) last_st[at + r] = r < nr && l != -INFINITY ? e.n - e.qlen + (r0 + r) / H : -1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_LSE + grp));
@@ -525,56 +527,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int buf = t & 1, key = key0 + kl;
       if (!(ok = warp_wait_cta(bar(B_S_FULL + buf), (t >> 1) & 1, abort_flag, a.status))) return 0.f;
       tc_fence_after();
-      uint64_t s2[2] = {0ull, 0ull};
-      float s1 = 0.f;
-      for (int cb = halves ? grp : 0; 32 * cb < nr; cb += halves ? 2 : 1) {
-        uint32_t sv[32];
-        tmem_ld32(tmem + tl + 256u * buf + 32u * cb, sv);
-        tmem_wait_ld();
-        if (spread) {
+      // A row whose lse is -inf adds 0 even where its q holds anything: where its
+      // scores made the sum a NaN, a second pass leaves it out. (The question costs
+      // 121.8 -> 122.9 us on 16..32 tokens x 64 heads over FP16 keys; a flag beside
+      // the staged constants 202 -> 217 on 8 tokens x 64 heads over FP8 keys.)
+      auto add_up = [&](auto leave_out) -> float {
+        uint64_t s2[2] = {0ull, 0ull};
+        float s1 = 0.f;
+        for (int cb = halves ? grp : 0; 32 * cb < nr; cb += halves ? 2 : 1) {
+          uint32_t sv[32];
+          tmem_ld32(tmem + tl + 256u * buf + 32u * cb, sv);
+          tmem_wait_ld();
+          if (spread) {
 #pragma unroll 1
-          for (int part = 1; part < kParts; ++part) {
-            uint32_t more[32];
-            tmem_ld32(tmem + tl + 256u * buf + (uint32_t)(kPartCols * part) + 32u * cb, more);
-            tmem_wait_ld();
+            for (int part = 1; part < kParts; ++part) {
+              uint32_t more[32];
+              tmem_ld32(tmem + tl + 256u * buf + (uint32_t)(kPartCols * part) + 32u * cb, more);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sv[i] = __float_as_uint(__uint_as_float(sv[i]) + __uint_as_float(more[i]));
+              for (int i = 0; i < 32; ++i) sv[i] = __float_as_uint(__uint_as_float(sv[i]) + __uint_as_float(more[i]));
+            }
+          }
+          const float* lr = lse_st + at + 32 * cb;
+          if (open && 32 * cb + 32 <= nr) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(lr + i);
+              float x0, x1, x2, x3;
+              f2_unpack(
+                  fma_f32x2(f2_pack(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), sl2x2, f2_pack(l.x, l.y)), x0,
+                  x1);
+              f2_unpack(
+                  fma_f32x2(f2_pack(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), sl2x2, f2_pack(l.z, l.w)),
+                  x2, x3);
+              if constexpr (decltype(leave_out)::value) {
+                x0 = l.x == -INFINITY ? -INFINITY : x0;
+                x1 = l.y == -INFINITY ? -INFINITY : x1;
+                x2 = l.z == -INFINITY ? -INFINITY : x2;
+                x3 = l.w == -INFINITY ? -INFINITY : x3;
+              }
+              s2[0] = add_f32x2(s2[0], f2_pack(ex2_approx(x0), ex2_approx(x1)));
+              s2[1] = add_f32x2(s2[1], f2_pack(ex2_approx(x2), ex2_approx(x3)));
+            }
+          } else {
+            const int* la = last_st + at + 32 * cb;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int last = la[i];
+              const bool sees = key <= last && (key > last - W || key < sinks);
+              const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), sl2, lr[i]));
+              s1 += sees ? x : 0.f;
+            }
           }
         }
-        const float* lr = lse_st + at + 32 * cb;
-        if (open && 32 * cb + 32 <= nr) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(lr + i);
-            float x0, x1, x2, x3;
-            f2_unpack(fma_f32x2(f2_pack(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), sl2x2, f2_pack(l.x, l.y)),
-                      x0, x1);
-            f2_unpack(
-                fma_f32x2(f2_pack(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), sl2x2, f2_pack(l.z, l.w)),
-                x2, x3);
-            s2[0] = add_f32x2(s2[0], f2_pack(ex2_approx(x0), ex2_approx(x1)));
-            s2[1] = add_f32x2(s2[1], f2_pack(ex2_approx(x2), ex2_approx(x3)));
-          }
-        } else {
-          const int* la = last_st + at + 32 * cb;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int last = la[i];
-            const bool sees = key <= last && (key > last - W || key < sinks);
-            const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), sl2, lr[i]));
-            s1 += sees ? x : 0.f;
-          }
-        }
-      }
+        float y0, y1, y2, y3;
+        f2_unpack(s2[0], y0, y1);
+        f2_unpack(s2[1], y2, y3);
+        return ((y0 + y1) + (y2 + y3)) + s1;
+      };
+      float sum = add_up(std::false_type{});
+      if (__any_sync(0xffffffffu, sum != sum)) sum = add_up(std::true_type{});
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(bar(B_S_EMPTY + buf)); else mbar_arrive_remote_relaxed(lead(B_S_EMPTY + buf));
       }
-      float y0, y1, y2, y3;
-      f2_unpack(s2[0], y0, y1);
-      f2_unpack(s2[1], y2, y3);
-      return ((y0 + y1) + (y2 + y3)) + s1;
+      return sum;
     };
     // this thread's key of a tile: its old weight and its page's table entry,
     // read one tile ahead

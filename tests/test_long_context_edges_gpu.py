@@ -47,3 +47,32 @@ def test_a_length_above_a_prefill_plans_is_computed_with_sinks_too(cuda_device, 
     o, l, tol, ltol = ref.attention(g, 800, 4)
     ref.close(out.reshape(o.shape), o, tol, "out")
     ref.close(lse.reshape(l.shape), l, ltol, "lse")
+
+
+# (T, H, dtype, window): every form of the tensor-core kernel, by type and rows per entry
+FORMS = [(1, 16, "bf16", 0), (2, 50, "fp16", 0), (4, 32, "fp8", 0), (2, 90, "fp8", 0), (2, 100, "bf16", 0),
+         (5, 128, "fp8", 0), (5, 128, "fp16", 0), (5, 128, "bf16", 150), (3, 65, "fp8", 150)]
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+@pytest.mark.parametrize("T,H,dtype,window", FORMS)
+def test_rows_left_out_by_their_lse_add_nothing_whatever_they_hold(cuda_device, T, H, dtype, window, kernel):
+    """Padding rows of a step: lse set to -inf, q never written (NaN here), also where every row sees every key."""
+    g = make_inputs_custom(2, T, H, dtype, [900, 333], seed=92, pool=1.5).to(cuda_device)
+    dec = mla.MlaDecoder(2, T, H, 900, dtype, cuda_device, kernel=kernel, window=window, sinks=4 if window else 0)
+    _, lse = dec(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, g.q_scale, g.kv_scale)
+    left = torch.zeros(2, T, H, dtype=torch.bool, device=cuda_device)
+    left[0, 0, 3] = left[1, T - 1, H - 1] = left[1, 0, H // 2] = True
+    lse = lse.view(2, T, H).masked_fill(left, -math.inf)
+    q = g.q.clone().view(torch.uint8)
+    q.view(2, T, H, -1)[left] = 0xFF  # a NaN in every type
+
+    def weights(rows):
+        return dec.key_weights(rows, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse,
+                               torch.zeros(2, 900, device=cuda_device), q_scale=g.q_scale, kv_scale=g.kv_scale)
+
+    got = weights(q.view(g.q.dtype).view(g.q.shape))
+    assert dec.status() == 0
+    want, tol = ref.key_weights(g, lse.reshape(-1, H), None, 1.0, 900, window, 4 if window else 0)
+    ref.close(got, want, tol, f"{kernel} {dtype} {T * H} rows")
+    assert torch.equal(got, weights(g.q))  # the same bits as with numbers there
