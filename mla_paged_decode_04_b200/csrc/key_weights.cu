@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
 
 cudaError_t launch_key_weights_simt(const KeyWeightArgs& k, cudaStream_t stream) {
   const mla_plan& p = k.a.plan;
-  const int64_t keys = min((int64_t)k.a.max_pages_per_seq * kTileKeys, (int64_t)p.max_seq_len + kTileKeys);
+  // as far as effective_seq_len lets a length go: the plan's splits may reach past its longest sequence
+  const int64_t keys = min((int64_t)k.a.max_pages_per_seq * kTileKeys, (int64_t)p.split_kv * p.keys_per_split);
   const int tiles = (int)((keys + kTileKeys - 1) / kTileKeys);
   const int64_t grid = (int64_t)p.batch * tiles;
   if (grid == 0) return cudaSuccess;

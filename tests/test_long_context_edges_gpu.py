@@ -76,3 +76,21 @@ def test_rows_left_out_by_their_lse_add_nothing_whatever_they_hold(cuda_device, 
     want, tol = ref.key_weights(g, lse.reshape(-1, H), None, 1.0, 900, window, 4 if window else 0)
     ref.close(got, want, tol, f"{kernel} {dtype} {T * H} rows")
     assert torch.equal(got, weights(g.q))  # the same bits as with numbers there
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+def test_key_weights_reach_as_far_as_a_length_above_the_plans(cuda_device, kernel, dtype):
+    """A plan for 640 keys whose splits (three of four pages) reach to 768: every key that the attention saw gets its
+    weight."""
+    lens = [768, 705, 640]
+    g = make_inputs_custom(3, 2, 32, dtype, lens, seed=93, pool=1.5).to(cuda_device)
+    dec = mla.MlaDecoder(3, 2, 32, 640, dtype, cuda_device, kernel=kernel, split_kv=3)
+    _, lse = dec(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, g.q_scale, g.kv_scale)
+    assert dec.status() == mla.MLA_DEV_SEQ_TOO_LONG
+    got = dec.key_weights(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale, lse,
+                          torch.zeros(3, 768, device=cuda_device), q_scale=g.q_scale, kv_scale=g.kv_scale)
+    assert dec.status() == mla.MLA_DEV_SEQ_TOO_LONG
+    want, tol = ref.key_weights(g, lse.reshape(-1, 32), None, 1.0, 768)
+    ref.close(got, want, tol, f"{kernel} {dtype}")
+    assert (got[0] > 0).all() and (got[1, :705] > 0).all()
