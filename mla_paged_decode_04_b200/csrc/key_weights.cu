@@ -6,8 +6,11 @@
 // rebuilt from its log-sum-exp, so one pass over K is enough and no maximum is
 // kept. One CTA per (entry, 64-key page), one warp per key at a time: lanes
 // split the 576 dims, the key's row stays in registers and the entry's query
-// rows are read one after the other. The sum runs over rows in order, in fp32
-// (at most a few thousand terms of at most 1).
+// rows are read one after the other. The sum runs over rows in order, in 64
+// bits: a prefill step has up to 131,072 rows (1024 tokens x 128 heads), over
+// which an fp32 sum of nearly equal terms drifts (1.2e-4 of the sum on uniform
+// attention over 4024 keys), and this form is what the tensor-core one, whose
+// partial sums are short, is held against.
 #include "device_common.cuh"
 
 namespace mla {
@@ -40,7 +43,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
     }
   }
   for (int j = key0 + warp; j < key1; j += 8) {
-    float sum = 0.f;
+    double sum = 0.;
     if (ok) {
       const int64_t base = ((int64_t)page * kTileKeys + (j - key0)) * MLA_D_QK;
       float kv[MLA_D_QK / 32];
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
     }
     if (lane == 0) {
       const float old = k.w_in ? k.decay * k.w_in[(int64_t)b * k.in_stride + j] : 0.f;
-      k.w_out[(int64_t)b * k.out_stride + j] = old + sum;
+      k.w_out[(int64_t)b * k.out_stride + j] = old + (float)sum;
     }
   }
 }

@@ -94,3 +94,27 @@ def test_key_weights_reach_as_far_as_a_length_above_the_plans(cuda_device, kerne
     want, tol = ref.key_weights(g, lse.reshape(-1, 32), None, 1.0, 768)
     ref.close(got, want, tol, f"{kernel} {dtype}")
     assert (got[0] > 0).all() and (got[1, :705] > 0).all()
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+def test_sums_over_very_many_rows(cuda_device, kernel):
+    """Uniform attention (q = 0, so scores are exactly 0) of 1024 new tokens of 128 heads: key j of n receives the sum
+    of 1 / (keys of the row) over the rows that see it, up to 131,072 nearly equal terms.
+
+    Bound: ex2's argument is lse * log2(e) rounded once from the given fp32 lse (at most log2(4024) < 12: half a step
+    2^-21, times ln 2) and ex2 is off by 2^-22: 6e-7 a term. The CUDA-core form adds in 64 bits and rounds once,
+    2^-24. The tensor-core form adds up to 64 terms in a register pair, then 3 parts, 512 row groups and 2 halves in
+    fp32: (64 + 3 + 512 + 2) * 2^-24 at most."""
+    new, pre, H = 1024, 3000, 128
+    n = new + pre
+    g = make_prefill_inputs([new], [pre], H, "bf16", seed=94).to(cuda_device)
+    g.q.zero_()
+    lse = torch.log(torch.arange(pre + 1, n + 1, device=cuda_device).double()).float()
+    dec = mla.MlaPrefill(1, new, H, n, "bf16", cuda_device, kernel=kernel)
+    got = dec.key_weights(g.q, g.cu_seqlens_q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale,
+                          lse[:, None].expand(new, H).contiguous(), torch.zeros(1, n, device=cuda_device))
+    assert dec.status() == 0
+    p = H * torch.exp(-lse.double())  # a token's rows on each key it sees
+    want = torch.cat([p.sum().expand(pre + 1), p.flip(0).cumsum(0).flip(0)[1:]])
+    rel = 6e-7 + (1 if kernel == "simt" else 581) * 2.0 ** -24
+    ref.close(got[0], want, rel * want, kernel)
