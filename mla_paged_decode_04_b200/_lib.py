@@ -471,7 +471,24 @@ def alloc_workspace(plan: MlaPlan, device) -> torch.Tensor:
     return torch.zeros(int(plan.workspace_bytes), dtype=torch.uint8, device=device)
 
 
-class MlaDecoder:
+class _WithWorkspace:
+    """The workspace of a plan (it may be replaced by another of the plan's size) and its status word."""
+
+    @property
+    def workspace(self) -> torch.Tensor:
+        return self._workspace
+
+    @workspace.setter
+    def workspace(self, workspace: torch.Tensor) -> None:
+        self._workspace = workspace
+        # the status word, where every kernel of this object reports
+        self._status = None if workspace is None else workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
+
+    def status(self, clear=True) -> int:
+        return mla_decode_status(self.workspace, clear)
+
+
+class MlaDecoder(_WithWorkspace):
     """Plan + workspace for one decode shape; call it once per decode step."""
 
     def __init__(self, batch, q_len, num_heads, max_seq_len, dtype, device, split_kv=0, fold=0,
@@ -484,7 +501,6 @@ class MlaDecoder:
             mla_decode_plan_sinks(self.plan, sinks)
         self.device = torch.device(device)
         self.workspace = alloc_workspace(self.plan, self.device)
-        self._status = self.workspace[:4].view(torch.int32)  # the status word
         self.batch, self.q_len, self.num_heads = batch, q_len, num_heads
 
     def __call__(self, q, kv_cache, block_tables, seq_lens, softmax_scale, q_scale=1.0,
@@ -505,11 +521,8 @@ class MlaDecoder:
         return key_weights(self.plan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, self._status,
                            weights, decay, q_scale, kv_scale, stream=stream)
 
-    def status(self, clear=True) -> int:
-        return mla_decode_status(self.workspace, clear)
 
-
-class MlaPrefill:
+class MlaPrefill(_WithWorkspace):
     """Plan + workspace for one ragged prefill shape (batch, longest entry, H, longest sequence)."""
 
     def __init__(self, batch, max_q_len, num_heads, max_seq_len, dtype, device, split_kv=0, fold=0,
@@ -521,7 +534,6 @@ class MlaPrefill:
             mla_decode_plan_sinks(self.plan, sinks)
         self.device = torch.device(device)
         self.workspace = alloc_workspace(self.plan, self.device)
-        self._status = self.workspace[:4].view(torch.int32)  # the status word
         self.num_heads = num_heads
 
     def __call__(self, q, cu_seqlens_q, kv_cache, block_tables, seq_lens, softmax_scale, q_scale=1.0,
@@ -541,6 +553,3 @@ class MlaPrefill:
         problems show in status()."""
         return key_weights(self.plan, q, kv_cache, block_tables, seq_lens, softmax_scale, lse, out, self._status,
                            weights, decay, q_scale, kv_scale, cu_seqlens_q, stream=stream)
-
-    def status(self, clear=True) -> int:
-        return mla_decode_status(self.workspace, clear)

@@ -118,3 +118,14 @@ def test_sums_over_very_many_rows(cuda_device, kernel):
     want = torch.cat([p.sum().expand(pre + 1), p.flip(0).cumsum(0).flip(0)[1:]])
     rel = 6e-7 + (1 if kernel == "simt" else 581) * 2.0 ** -24
     ref.close(got[0], want, rel * want, kernel)
+
+
+def test_key_weights_report_in_a_workspace_that_was_put_in_place_of_the_first(cuda_device):
+    g = make_inputs_custom(2, 1, 32, "bf16", [300, 200], seed=6, pool=1.5).to(cuda_device)
+    dec, other = (mla.MlaDecoder(2, 1, 32, 300, "bf16", cuda_device) for _ in range(2))
+    dec.workspace = other.workspace
+    _, lse = dec(g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+    tables = g.block_tables.clone()
+    tables[0, 1] = -1
+    dec.key_weights(g.q, g.kv_cache, tables, g.seq_lens, g.softmax_scale, lse, torch.zeros(2, 300, device=cuda_device))
+    assert dec.status() == mla.MLA_DEV_BAD_PAGE
