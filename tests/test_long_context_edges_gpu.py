@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import long_context_ref as ref
+import long_context_tight as tight
 import mla_paged_decode_04_b200 as mla
 from mla_paged_decode_04_b200.inputs import make_inputs_custom, make_prefill_inputs
 
@@ -129,3 +130,85 @@ def test_key_weights_report_in_a_workspace_that_was_put_in_place_of_the_first(cu
     tables[0, 1] = -1
     dec.key_weights(g.q, g.kv_cache, tables, g.seq_lens, g.softmax_scale, lse, torch.zeros(2, 300, device=cuda_device))
     assert dec.status() == mla.MLA_DEV_BAD_PAGE
+
+
+# decode (T, H, dtype, seq_lens) or ragged (new, prefix, H, dtype): each form of the kernel, groups that end inside 32
+# columns, a window with sinks
+TIGHT = [
+    ((4, 32, "bf16", [900, 70]), 0, 0),
+    ((1, 33, "fp16", [700, 129]), 0, 0),
+    ((2, 100, "fp8", [600, 257]), 0, 0),                       # 200 rows of FP8
+    ((2, 120, "fp16", [515, 256]), 0, 0),                      # 240 rows of 16 bits
+    ((3, 115, "fp8", [700, 300]), 0, 0),                       # 345 rows of FP8: two groups
+    ((5, 128, "bf16", [513, 300]), 0, 0),
+    (([130, 3, 64], [250, 900, 1], 20, "fp8"), 0, 0),          # 2600 rows an entry
+    (([130, 3, 64], [250, 900, 1], 20, "fp16"), 0, 0),
+    (([70, 41], [600, 333], 128, "fp8"), 90, 66),              # 8960 rows
+    (([70, 41], [600, 333], 128, "bf16"), 90, 66),
+]
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+@pytest.mark.parametrize("case", range(len(TIGHT)))
+def test_key_weights_within_a_bound_that_a_lost_row_breaks(cuda_device, case, kernel):
+    shape, window, sinks = TIGHT[case]
+    if isinstance(shape[0], int):
+        T, H, dtype, lens = shape
+        g = make_inputs_custom(len(lens), T, H, dtype, lens, seed=95 + case, pool=1.5).to(cuda_device)
+        dec = mla.MlaDecoder(len(lens), T, H, g.max_seq_len, dtype, cuda_device, kernel=kernel, window=window,
+                             sinks=sinks)
+        args = (g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+    else:
+        new, prefix, H, dtype = shape
+        g = make_prefill_inputs(new, prefix, H, dtype, seed=95 + case).to(cuda_device)
+        dec = mla.MlaPrefill(len(new), max(new), H, g.max_seq_len, dtype, cuda_device, kernel=kernel, window=window,
+                             sinks=sinks)
+        args = (g.q, g.cu_seqlens_q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+    _, lse = dec(*args, g.q_scale, g.kv_scale)
+    got = dec.key_weights(*args, lse, torch.zeros(g.batch, g.max_seq_len, device=cuda_device), q_scale=g.q_scale,
+                          kv_scale=g.kv_scale)
+    assert dec.status() == 0
+    want, tol, rows = tight.key_weights(g, lse.reshape(-1, H), g.max_seq_len, window, sinks)
+    ref.close(got, want, tol, f"{kernel} case {case}")
+    for b, p in enumerate(rows):  # without any one of its rows an entry would be out of bounds somewhere
+        assert p is None or (p > 2 * tol[b, :p.shape[1]]).any(1).all()
+
+
+def test_16_bit_scores_of_few_rows_lose_less_to_cut_sums(cuda_device):
+    """The tensor cores cut partial sums toward zero, at a unit of their own size. Scores of at most 64 rows go to four
+    accumulators. With positive q and k (64-dim chunks of about 36, 3 + 2 + 2 + 2 of them an accumulator) the units
+    met on the way add up to a quarter of one accumulator's: 13.7 against 3.6 units of 2^-24 of the score, whatever
+    share of a unit an addition loses. So the mean loss has to be less than half that of 96 rows, which have one."""
+    n, scale = 4096, 30 / 324
+    gen = torch.Generator(device=cuda_device).manual_seed(7)
+    positive = lambda *s: (0.5 + 0.5 * torch.rand(*s, generator=gen, device=cuda_device)).half()  # noqa: E731
+    k, q = positive(n // 64, 64, 576), positive(1, 1, 1, 576)
+    tables = torch.arange(n // 64, dtype=torch.int32, device=cuda_device)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=cuda_device)
+    s = (k.view(n, 576).double() @ q.view(576).double()) * scale
+    lost = []
+    for heads in (1, 64, 96):
+        lse = torch.full((1, 1, heads), -math.inf, device=cuda_device)
+        lse[0, 0, 0] = 30.0  # one row counts
+        dec = mla.MlaDecoder(1, 1, heads, n, "fp16", cuda_device)
+        w = dec.key_weights(q.expand(1, 1, heads, 576).contiguous(), k, tables, lens, scale, lse,
+                            torch.zeros(1, n, device=cuda_device))
+        lost.append(float((s - 30.0 - w[0].double().log()).mean()))
+    assert 0 < lost[0] < lost[2] / 2 and 0 < lost[1] < lost[2] / 2, lost
+
+
+def test_evicted_weights_arrive_with_every_bit(cuda_device):
+    """NaN among the weights: what is gathered is compared by its bits (NaN differs from itself)."""
+    lens, budget, sinks, recent = [1000, 777, 3000], 200, 3, 20
+    g = make_inputs_custom(3, 1, 1, "fp16", lens, seed=17, pool=1.2).to(cuda_device)
+    w = torch.randn(3, 3000, generator=torch.Generator().manual_seed(1))
+    w = torch.where(w > -1.2, math.nan, w).to(cuda_device)
+    per = (budget + 63) // 64
+    out_cache = torch.zeros(3 * per, 64, 576, dtype=torch.float16, device=cuda_device)
+    out_tables = torch.arange(3 * per, dtype=torch.int32, device=cuda_device).view(3, per)
+    _, kept, out_w = mla.cache_evict(w, g.seq_lens, g.kv_cache, g.block_tables, out_cache, out_tables, budget, sinks,
+                                     recent)
+    for b, want in enumerate(ref.evict(w, lens, budget, sinks, recent)):
+        assert kept[b].tolist() == want
+        assert torch.equal(out_w[b].view(torch.int32), w[b, want].view(torch.int32))
+        assert torch.isnan(out_w[b]).any() and not torch.isnan(out_w[b]).all()
