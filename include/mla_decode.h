@@ -76,8 +76,9 @@ typedef enum {
 #define MLA_DEV_BAD_QLEN 0x8     /* ragged queries: a cu_seqlens_q range decreasing, longer than the
                                     plan's max_q_len or past total_q; that entry gets no output */
 #define MLA_DEV_BOUNDS 0x10      /* bounds-checking build only (mla_bounds_checked): a global
-                                    index of the CTA-pair or combine kernels fell outside its
-                                    buffer; that access was skipped, outputs unspecified */
+                                    index of the CTA-pair, combine, key-weight or eviction
+                                    kernels fell outside its buffer; that access was skipped,
+                                    outputs unspecified */
 
 typedef enum {
   MLA_KERNEL_AUTO = 0,         /* MLA_KERNEL_TCGEN05 */

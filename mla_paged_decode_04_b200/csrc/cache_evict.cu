@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kSelThreads = 512;  // 1024 leave one CTA an SM: of 16 clusters of 8 half waited for the others
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelPerSM = MLA_BOUNDS_CHECK ? 1 : 2;  // (the checks take more than 64 registers)
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxHeld = 48 * 1024;  // numbers a CTA keeps in shared memory; of longer stretches none
@@ -47,6 +48,18 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
   if (w != w) return 0u;
   const uint32_t b = w == 0.f ? 0u : __float_as_uint(w);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// Bounds check of the checking build (see in_bounds): whether i lies in [0, n).
+__device__ __forceinline__ bool evict_in_bounds(const EvictArgs& e, int64_t i, int64_t n) {
+#if MLA_BOUNDS_CHECK
+  if (i >= 0 && i < n) return true;
+  if (e.status) atomicOr(e.status, MLA_DEV_BOUNDS);
+  return false;
+#else
+  (void)e, (void)i, (void)n;
+  return true;
+#endif
 }
 
 __device__ __forceinline__ int evict_len(const EvictArgs& e, int b, bool flag) {
@@ -84,6 +97,7 @@ __device__ __forceinline__ void move_step(const EvictArgs& e, int b, int it, int
   constexpr int kRows = 32 * kMoveChunks / kPer;        // rows of a step
   static_assert(32 * kMoveChunks % kPer == 0 && kTileKeys % kRows == 0, "whole rows, within a page");
   const int lane = threadIdx.x & 31, i0 = it * kRows;
+  if (!evict_in_bounds(e, b, e.batch) || !evict_in_bounds(e, i0 / kTileKeys, e.out_max_pages_per_seq)) return;
   const int to = e.out_block_tables[(int64_t)b * e.out_max_pages_per_seq + i0 / kTileKeys];
   if (to < 0 || (int64_t)to >= e.out_num_pages) {
     if (e.status && lane == 0) atomicOr(e.status, MLA_DEV_BAD_PAGE);
@@ -92,9 +106,10 @@ __device__ __forceinline__ void move_step(const EvictArgs& e, int b, int it, int
   // lane r: the source row of row i0 + r, or -1 (past the length, or on a page
   // outside the cache: zeros arrive)
   int64_t from = -1;
-  if (lane < kRows && i0 + lane < len) {
+  if (lane < kRows && i0 + lane < len && evict_in_bounds(e, i0 + lane, e.budget)) {
     const int j = e.kept[(int64_t)b * e.budget + i0 + lane];
-    const int pg = e.block_tables[(int64_t)b * e.max_pages_per_seq + j / kTileKeys];
+    const bool in_table = evict_in_bounds(e, j, (int64_t)e.max_pages_per_seq * kTileKeys);
+    const int pg = in_table ? e.block_tables[(int64_t)b * e.max_pages_per_seq + j / kTileKeys] : -1;
     if (pg < 0 || (int64_t)pg >= e.num_pages) {
       if (e.status) atomicOr(e.status, MLA_DEV_BAD_PAGE);
     } else {
@@ -136,7 +151,7 @@ __global__ void __launch_bounds__(256) cache_evict_move_kernel(const EvictArgs e
 // held: room for the weights of a CTA's stretch (0: read them again at each
 // use). kRowBytes > 0: the cluster moves its entry's rows too.
 template <bool kCluster, int kRowBytes>
-__global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(const EvictArgs e, int ctas_arg, int held) {
+__global__ void __launch_bounds__(kSelThreads, kSelPerSM) cache_evict_select_kernel(const EvictArgs e, int ctas_arg, int held) {
   extern __shared__ __align__(16) uint32_t held_u[];
   __shared__ __align__(16) int hist[3][kBins];
   __shared__ __align__(16) int share[kCluster ? kBins / 2 : 4];      // this CTA's bins, summed over the cluster
@@ -157,9 +172,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
   const int n = evict_len(e, b, tid == 0 && rank == 0);
   const int len = min(n, e.budget);
   const float* w = e.weights + (int64_t)b * e.weights_stride;
+  auto weight_at = [&](int j) -> float { return evict_in_bounds(e, j, e.cols) ? w[j] : 0.f; };
   int32_t* kept = e.kept + (int64_t)b * e.budget;
   float* ow = e.out_weights ? e.out_weights + (int64_t)b * e.out_weights_stride : nullptr;
   auto keep = [&](int i, int j, float x) {
+    if (!evict_in_bounds(e, i, e.budget)) return;
     kept[i] = j;
     if (ow) ow[i] = x;
   };
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
   if (n <= e.budget) {
     for (int i = rank * kSelThreads + tid; i < e.budget; i += ctas * kSelThreads) {
       if (i < n)
-        keep(i, i, w[i]);
+        keep(i, i, weight_at(i));
       else
         kept[i] = -1;
     }
@@ -191,14 +208,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
   auto keep_safe = [&](int i, float x) {
     if (i < e.sinks) keep(i, i, x); else keep(k + i, hi + i - e.sinks, x);
   };
-  auto safe_weight = [&](int i) -> float { return w[i < e.sinks ? i : hi + i - e.sinks]; };
+  auto safe_weight = [&](int i) -> float { return weight_at(i < e.sinks ? i : hi + i - e.sinks); };
   const int safe0 = rank * kSelThreads + tid;
   const float x_safe = safe0 < safe ? safe_weight(safe0) : 0.f;  // (its store comes after the loads below)
   // this CTA's stretch [c0, c1) of the candidates
   const int per_cta = (hi - lo + ctas - 1) / ctas;
   const int c0 = min(hi, lo + rank * per_cta), c1 = min(hi, c0 + per_cta);
   const bool hold = c1 - c0 <= held;
-  auto number = [&](int j) -> uint32_t { return hold ? held_u[j - c0] : weight_order(w[j]); };
+  auto number = [&](int j) -> uint32_t { return hold ? held_u[j - c0] : weight_order(weight_at(j)); };
   if (k > 0) {
     __syncthreads();  // the histograms are zero
     constexpr int kAhead = 12;  // loads in flight per thread
@@ -207,7 +224,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int j = jb + i * kSelThreads + tid;
-        x[i] = j < c1 ? w[j] : 0.f;
+        x[i] = j < c1 ? weight_at(j) : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
         }
         if (4 * n4 + tid < c1 - c0) count(held_u[4 * n4 + tid]);
       } else {
-        for (int j = c0 + tid; j < c1; j += kSelThreads) count(weight_order(w[j]));
+        for (int j = c0 + tid; j < c1; j += kSelThreads) count(weight_order(weight_at(j)));
       }
     }
   }
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     const int base = e.sinks + gt0 + min(eq0, ties);
     for (int i = lane; i < count; i += 32) {
       const int j = (int)list[i];
-      keep(base + i, j, w[j]);
+      keep(base + i, j, weight_at(j));
     }
   } else {
     for (int j = j0 + lane; j - lane < j1; j += 32) {
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
       const unsigned before = (1u << lane) - 1u;
       const int eq_before = eq0 + __popc(q & before);
       if (((g >> lane) & 1u) || (((q >> lane) & 1u) && eq_before < ties))
-        keep(e.sinks + gt0 + __popc(g & before) + min(eq_before, ties), j, w[j]);
+        keep(e.sinks + gt0 + __popc(g & before) + min(eq_before, ties), j, weight_at(j));
       gt0 += __popc(g);
       eq0 += __popc(q);
     }

@@ -34,13 +34,11 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
   const int first_last = n - e.qlen;  // newest key of the entry's first token
   const bool seen = e.qlen > 0 && key0 < n && (key1 > row_key_lo(p, first_last) || key0 < sinks);
   int page = 0;
-  bool ok = seen;
-  if (seen) {
+  bool ok = false;
+  if (seen && in_bounds(a, b, p.batch) && in_bounds(a, tile, a.max_pages_per_seq)) {
     page = a.block_tables[(int64_t)b * a.max_pages_per_seq + tile];
-    if (page < 0 || (int64_t)page >= a.num_pages) {
-      ok = false;
-      if (threadIdx.x == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
-    }
+    ok = page >= 0 && (int64_t)page < a.num_pages;
+    if (!ok && threadIdx.x == 0) atomicOr(a.status, MLA_DEV_BAD_PAGE);
   }
   for (int j = key0 + warp; j < key1; j += 8) {
     double sum = 0.;
@@ -54,6 +52,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
         if (j > last || (j < row_key_lo(p, last) && j >= sinks)) continue;
         for (int h = 0; h < p.num_heads; ++h) {
           const int64_t row = (e.q0 + t) * p.num_heads + h;
+          if (!in_bounds(a, row, out_rows(a))) continue;
           const float lse = k.lse[row];
           if (lse == -INFINITY) continue;
           float dot = 0.f;
@@ -64,7 +63,7 @@ __global__ void __launch_bounds__(256) key_weights_simt_kernel(const KeyWeightAr
         }
       }
     }
-    if (lane == 0) {
+    if (lane == 0 && in_bounds(a, b, p.batch) && in_bounds(a, j, k.cols)) {
       const float old = k.w_in ? k.decay * k.w_in[(int64_t)b * k.in_stride + j] : 0.f;
       k.w_out[(int64_t)b * k.out_stride + j] = old + (float)sum;
     }

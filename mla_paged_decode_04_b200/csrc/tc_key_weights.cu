@@ -218,7 +218,13 @@ __device__ __forceinline__ void load_rows(const KeyWeightParams& prm, uint32_t d
 // 0. Read a tile ahead of its use.
 __device__ __forceinline__ int key_entry(const DecodeArgs& a, const Entry& e, int key) {
   if (!page_seen(key, e.klo, e.n, sinks_of(a.plan))) return 0;
+  if (!in_bounds(a, e.b, a.plan.batch) || !in_bounds(a, key / kTileKeys, a.max_pages_per_seq)) return 0;
   return ld_nc_ordered(a.block_tables + (int64_t)e.b * a.max_pages_per_seq + key / kTileKeys);
+}
+// Whether key `key` of entry b has a place among the weights (the checking
+// build; both arrays have [batch] rows of `cols`).
+__device__ __forceinline__ bool weight_in_bounds(const KeyWeightArgs& k, int b, int64_t key) {
+  return in_bounds(k.a, b, k.a.plan.batch) && in_bounds(k.a, key, k.cols);
 }
 __device__ __forceinline__ bool page_valid(const DecodeArgs& a, int pg) { return pg >= 0 && (int64_t)pg < a.num_pages; }
 // an entry outside the cache reads page 0 (the sums leave its keys out)
@@ -461,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float* in = prm.k.w_in ? prm.k.w_in + (int64_t)e.b * prm.k.in_stride : nullptr;
         float* out = prm.k.w_out + (int64_t)e.b * prm.k.out_stride;
         for (int64_t j = k0 + 32 * (w_id % parts) + lane; j < k1; j += 32 * parts)
-          out[j] = in ? prm.k.decay * in[j] : 0.f;
+          if (weight_in_bounds(prm.k, e.b, j)) out[j] = in ? prm.k.decay * in[j] : 0.f;
       }
     }
   } else {
@@ -493,7 +499,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int r = own_row(u);
-        x.l[u] = (u == 0 || !halves) && r < nr ? prm.k.lse[e.q0 * H + r0 + r] : -INFINITY;
+        const int64_t row = e.q0 * H + r0 + r;
+        x.l[u] = (u == 0 || !halves) && r < nr && in_bounds(a, row, out_rows(a)) ? prm.k.lse[row] : -INFINITY;
       }
       return x;
     };
@@ -603,7 +610,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto ahead = [&](const Entry& e, int key0) -> Ahead {
       Ahead h;
       const int key = key0 + kl;
-      h.old = prm.k.w_in && key < e.n && key < prm.k.cols ? prm.k.w_in[(int64_t)e.b * prm.k.in_stride + key] : 0.f;
+      h.old = prm.k.w_in && key < e.n && key < prm.k.cols && weight_in_bounds(prm.k, e.b, key)
+                  ? prm.k.w_in[(int64_t)e.b * prm.k.in_stride + key] : 0.f;
       h.entry = key_entry(a, e, key0 + (kl & ~(kTileKeys - 1)));
       return h;
     };
@@ -613,7 +621,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return false;
     };
     auto write = [&](const Entry& e, int key, float old, float sum) {
-      if (key < e.n && key < prm.k.cols) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = prm.k.decay * old + sum;
+      if (key < e.n && key < prm.k.cols && weight_in_bounds(prm.k, e.b, key))
+        prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = prm.k.decay * old + sum;
     };
     auto tile_key = [&]() -> int { return kTile * w.tile(p) + kHalf * (int)rank; };
 

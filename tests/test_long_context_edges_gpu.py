@@ -8,6 +8,7 @@ import torch
 import long_context_ref as ref
 import long_context_tight as tight
 import mla_paged_decode_04_b200 as mla
+from mla_paged_decode_04_b200 import _lib
 from mla_paged_decode_04_b200.inputs import make_inputs_custom, make_prefill_inputs
 
 pytestmark = pytest.mark.gpu
@@ -212,3 +213,43 @@ def test_evicted_weights_arrive_with_every_bit(cuda_device):
         assert kept[b].tolist() == want
         assert torch.equal(out_w[b].view(torch.int32), w[b, want].view(torch.int32))
         assert torch.isnan(out_w[b]).any() and not torch.isnan(out_w[b]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+def test_key_weights_and_eviction_through_the_bounds_checking_build(cuda_device, dtype, kernel, monkeypatch):
+    """No check fires on valid calls, and the results are the normal build's, bit for bit."""
+    long = torch.rand(2, 12000, generator=torch.Generator().manual_seed(3)).to(cuda_device)
+
+    def run():
+        res = []
+        for T, H, lens, window, sinks in ((4, 32, [1000, 391, 0], 0, 0), (3, 100, [700, 65, 1], 90, 66)):
+            g = make_inputs_custom(3, T, H, dtype, lens, seed=96, pool=2.0).to(cuda_device)
+            dec = mla.MlaDecoder(3, T, H, 1000, dtype, cuda_device, kernel=kernel, window=window, sinks=sinks)
+            args = (g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+            _, lse = dec(*args, g.q_scale, g.kv_scale)
+            w = dec.key_weights(*args, lse, torch.zeros(3, 1000, device=cuda_device), q_scale=g.q_scale,
+                                kv_scale=g.kv_scale)
+            assert dec.status() == 0
+            out_cache = torch.zeros(16, 64, 576, device=cuda_device).to(g.kv_cache.dtype)
+            out_tables = torch.arange(15, dtype=torch.int32, device=cuda_device).view(3, 5)
+            status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+            got = mla.cache_evict(w, g.seq_lens, g.kv_cache, g.block_tables, out_cache, out_tables, 300, 4, 32,
+                                  device_status=status)
+            assert int(status) == 0
+            res += [w, out_cache.view(torch.uint8), *got]
+        # a cluster an entry
+        g = make_inputs_custom(2, 1, 1, dtype, [12000, 5], seed=97, pool=1.1).to(cuda_device)
+        out_cache = torch.zeros(8, 64, 576, device=cuda_device).to(g.kv_cache.dtype)
+        status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+        got = mla.cache_evict(long, g.seq_lens, g.kv_cache, g.block_tables, out_cache,
+                              torch.arange(8, dtype=torch.int32, device=cuda_device).view(2, 4), 200, 4, 32,
+                              device_status=status)
+        assert int(status) == 0
+        return res + [out_cache.view(torch.uint8), *got]
+
+    want = run()
+    monkeypatch.setattr(_lib, "_lib", _lib.load_library(_lib.CHECK_LIB_PATH))
+    assert mla.bounds_checked()
+    for a, b in zip(run(), want):
+        assert torch.equal(a, b)
