@@ -133,12 +133,13 @@ typedef struct {
   int32_t window;    /* sliding window in keys (0 = none); set with mla_decode_plan_window */
   int32_t varlen;    /* 1: ragged query lengths (mla_prefill_plan / mla_prefill), q_len = the longest */
   int32_t fault_test; /* 0, as the planner sets it. Tests of failure detection only: 1 makes the
-                         FP8 CTA-pair kernel leave the first tile of every pair unloaded, so that
-                         the wait for it runs out (MLA_DEV_TIMEOUT after its 0.5 s limit, no
-                         fault); 2, accepted by the bounds-checking build only, moves every
-                         output row and partial slot of that kernel past its buffer, so that
-                         the checks skip each store and set MLA_DEV_BOUNDS; refused on other
-                         plans */
+                         FP8 CTA-pair kernels (attention and mla_key_weights) leave the first
+                         tile of every pair unloaded, so that the wait for it runs out
+                         (MLA_DEV_TIMEOUT after its 0.5 s limit, no fault); 2, accepted by the
+                         bounds-checking build only, moves every output row and partial slot of
+                         the attention kernel, and every weight of a key that mla_key_weights
+                         sums, past its buffer, so that the checks skip each store and set
+                         MLA_DEV_BOUNDS; refused on other plans */
   int32_t sinks;     /* first keys that stay visible with a window (0 = none); set with
                         mla_decode_plan_sinks */
 } mla_plan;

@@ -335,14 +335,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (!(ok = bounded_wait_cta(bar(B_EMPTY + st), ph, abort_flag, a.status))) return;
-          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2u * (uint32_t)ring_rows * C::row_bytes(s));
-          const uint32_t sd = ring0 + st * C::kSlotBytes, full = full0 + 8u * st;
+          // failure-detection test mode (FP8 plans): the pair's first slot is never
+          // loaded, so the MMA issuer's wait for it runs out
+          if (!(E == 1 && p.fault_test == 1 && filled == 0)) {
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2u * (uint32_t)ring_rows * C::row_bytes(s));
+            const uint32_t sd = ring0 + st * C::kSlotBytes, full = full0 + 8u * st;
 #pragma unroll
-          for (int c = C::first(s); c < C::last(s); ++c) {
-            const uint32_t cd = sd + (c - C::first(s)) * kChunkBytes;
-            if (kForm != kKeysStay)
-              load_keys<C>(prm, cd, c, pg0, pg1, full, kForm == kRowsStay ? pol_once : pol_again);
-            if (kForm != kRowsStay) load_rows<C>(prm, cd + C::kRowsAt, c, row, full, pol_again);
+            for (int c = C::first(s); c < C::last(s); ++c) {
+              const uint32_t cd = sd + (c - C::first(s)) * kChunkBytes;
+              if (kForm != kKeysStay)
+                load_keys<C>(prm, cd, c, pg0, pg1, full, kForm == kRowsStay ? pol_once : pol_again);
+              if (kForm != kRowsStay) load_rows<C>(prm, cd + C::kRowsAt, c, row, full, pol_again);
+            }
           }
           ++filled;
           if (++st == NS) st = 0, ph ^= 1;
@@ -621,8 +625,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return false;
     };
     auto write = [&](const Entry& e, int key, float old, float sum) {
-      if (key < e.n && key < prm.k.cols && weight_in_bounds(prm.k, e.b, key))
-        prm.k.w_out[(int64_t)e.b * prm.k.out_stride + key] = prm.k.decay * old + sum;
+      if (key >= e.n || key >= prm.k.cols) return;
+      // (test mode 2 of the checking build: every store past its row, where the check skips it)
+      const int64_t at = key + (MLA_BOUNDS_CHECK && p.fault_test == 2 ? prm.k.cols : 0);
+      if (weight_in_bounds(prm.k, e.b, at)) prm.k.w_out[(int64_t)e.b * prm.k.out_stride + at] = prm.k.decay * old + sum;
     };
     auto tile_key = [&]() -> int { return kTile * w.tile(p) + kHalf * (int)rank; };
 

@@ -1,6 +1,7 @@
 """Edge calls of the long-context operators on the GPU: lengths above the plan's, rows that are left out, sums of very
 many rows, results packed into shared buffers. Plain 64-bit forms and bounds as in long_context_ref.py."""
 import math
+import time
 
 import pytest
 import torch
@@ -253,3 +254,53 @@ def test_key_weights_and_eviction_through_the_bounds_checking_build(cuda_device,
     assert mla.bounds_checked()
     for a, b in zip(run(), want):
         assert torch.equal(a, b)
+
+
+# (T, H): the forms of FP8 weights: up to 128 rows, up to 256, and more
+FP8_FORMS = [(4, 32), (2, 100), (3, 115)]
+
+
+@pytest.mark.parametrize("T,H", FP8_FORMS)
+def test_a_wait_of_key_weights_that_runs_out(cuda_device, T, H):
+    """A plan in its failure-detection mode: no pair loads its first ring slot, so the MMA issuer's wait for it ends
+    after its limit, every other role gives up in turn and the kernel returns with MLA_DEV_TIMEOUT. The next call on the
+    same buffers is clean."""
+    g = make_inputs_custom(2, T, H, "fp8", [3000, 1200], seed=98, pool=2.0).to(cuda_device)
+    dec = mla.MlaDecoder(2, T, H, 3000, "fp8", cuda_device)
+    args = (g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+    _, lse = dec(*args, g.q_scale, g.kv_scale)
+    w = torch.zeros(2, 3000, device=cuda_device)
+    kw = dict(q_scale=g.q_scale, kv_scale=g.kv_scale)
+    want = dec.key_weights(*args, lse, w.clone(), **kw)
+    torch.cuda.synchronize()
+    assert dec.status() == 0
+    faulty = type(dec.plan).from_buffer_copy(dec.plan)
+    faulty.fault_test = 1
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    t0 = time.perf_counter()
+    mla.key_weights(faulty, *args, lse, w, status, **kw)
+    torch.cuda.synchronize()
+    waited = time.perf_counter() - t0
+    assert int(status) == mla.MLA_DEV_TIMEOUT
+    assert 0.3 < waited < 20.0, waited
+    again = dec.key_weights(*args, lse, torch.zeros_like(want), **kw)
+    assert dec.status() == 0 and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("T,H", FP8_FORMS)
+def test_key_weights_past_their_rows_are_caught(cuda_device, T, H, monkeypatch):
+    """The checking build with the plan's second test mode: every weight would go past its row, and is not written."""
+    monkeypatch.setattr(_lib, "_lib", _lib.load_library(_lib.CHECK_LIB_PATH))
+    g = make_inputs_custom(2, T, H, "fp8", [900, 333], seed=99, pool=2.0).to(cuda_device)
+    dec = mla.MlaDecoder(2, T, H, 900, "fp8", cuda_device)
+    args = (g.q, g.kv_cache, g.block_tables, g.seq_lens, g.softmax_scale)
+    _, lse = dec(*args, g.q_scale, g.kv_scale)
+    wide = torch.full((3, 900), -3.0, device=cuda_device)  # a row more than the call is given
+    kw = dict(q_scale=g.q_scale, kv_scale=g.kv_scale)
+    faulty = type(dec.plan).from_buffer_copy(dec.plan)
+    faulty.fault_test = 2
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    mla.key_weights(faulty, *args, lse, wide[:2], status, **kw)
+    assert int(status) == mla.MLA_DEV_BOUNDS and (wide == -3.0).all()
+    dec.key_weights(*args, lse, wide[:2], **kw)
+    assert dec.status() == 0 and (wide[0] >= 0).all() and (wide[2] == -3.0).all()
