@@ -420,16 +420,17 @@ cudaError_t launch_select(const EvictArgs& e, cudaLaunchConfig_t& cfg, int ctas,
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t stream) {
-  // CTAs per entry: as many as the SMs hold at two each, with at least 1024
-  // candidates for each; one for tables of few keys, since a cluster's launch and
-  // barriers cost 4 to 5 us whatever its entry (16 entries of 2500 keys: 12.7 us
-  // with one, 16.8 with clusters; of 9000 15.3 and 19.5; of 20,000 20.5 and 19.8; 64 of
-  // 9000 68.2 and 65.8)
+  // CTAs per entry: one where the columns or the table hold fewer than 10,240
+  // keys, since a cluster's launch and barriers cost 4 to 5 us whatever its entry
+  // holds (16 entries of 2500 keys: 12.7 us with one, 16.8 with clusters; of 9000
+  // 15.3 and 19.5; of 20,000 20.5 and 19.8), else as many as the SMs hold at two
+  // each. The batch is not in the rule: many entries gain from clusters a little
+  // earlier (64 of 9000: 68.2 us with one, 65.8 with clusters).
   const int64_t longest = e.cols < (int64_t)e.max_pages_per_seq * kTileKeys ? e.cols
                                                                             : (int64_t)e.max_pages_per_seq * kTileKeys;
   int ctas = 1;
   constexpr int64_t kClusterKeys = 10240;
-  while (longest >= kClusterKeys && ctas < kMaxCluster && (int64_t)e.batch * ctas * 2 <= 2 * kNumSMs && longest >= 2048 * ctas) ctas *= 2;
+  while (longest >= kClusterKeys && ctas < kMaxCluster && (int64_t)e.batch * ctas <= kNumSMs) ctas *= 2;
   const int64_t stretch = (longest + ctas - 1) / ctas;
   const int held = stretch <= kMaxHeld ? (int)stretch : 0;
   // (64 entries, 256 CTAs: 64.5 us against 71.3 in two kernels; 16 entries, 128
