@@ -42,12 +42,16 @@
 // in half the time (16..32 last tokens x 64 heads over 4 x up to 32,768 FP16
 // keys: 127 -> 118 us; 16 x 4 tokens x 64 heads over 81,920 FP8 keys: 207 -> 194 us).
 //
-// Measured: 16 x 4 tokens x 32 heads over 81,920 FP8 keys 132 us in replayed
-// graphs (5.8 TB/s, 0.89 of the copy bandwidth; 158 us where the power limit
-// holds the clock down), 4 x 4 x 32 over 8192 BF16 keys 16 us (two tiles a pair,
-// 5.9 us of HBM time).
-// Every wait is bounded as in the attention kernels. No TMA load uses
-// multicast.
+// Measured: 16 x 4 tokens x 32 heads over 81,920 FP8 keys 123 to 135 us in
+// replayed graphs (5.7 to 6.2 TB/s, 0.87 to 0.95 of the copy bandwidth; 149 us
+// where the power limit holds the clock down), 4 x 4 x 32 over 8192 BF16 keys 16 us
+// (two tiles a pair, 5.9 us of HBM time). kKeysStay: 16 x 8 tokens x 64 heads over
+// 40,960 FP8 keys 204 us (117 of FP8 products at twice the BF16 rate; no unit is
+// full: tensor pipe 38 %, ex2 36 %, issue 27 % of the active cycles of a quarter of
+// it, so the hand-over between products and sums is what is left), 16..32 tokens x
+// 64 heads over 4 x up to 32,768 95 us (45 of products).
+// Every wait is bounded as in the attention kernels; a plan with fault_test = 1
+// makes them run out (tests). No TMA load uses multicast.
 #include <cuda.h>
 
 #include <type_traits>
