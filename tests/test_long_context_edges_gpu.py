@@ -304,3 +304,31 @@ def test_key_weights_past_their_rows_are_caught(cuda_device, T, H, monkeypatch):
     assert int(status) == mla.MLA_DEV_BOUNDS and (wide == -3.0).all()
     dec.key_weights(*args, lse, wide[:2], **kw)
     assert dec.status() == 0 and (wide[0] >= 0).all() and (wide[2] == -3.0).all()
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+def test_pages_past_32_bit_offsets(cuda_device, kernel):
+    """The same step on the last pages of a cache of 2.2e9 elements, and an eviction to the pages before them."""
+    lens, pages = [1500, 700, 300], 60000
+    g = make_inputs_custom(3, 4, 32, "bf16", lens, seed=101, pool=1.0).to(cuda_device)
+    big = torch.empty(pages, 64, 576, dtype=torch.bfloat16, device=cuda_device)
+    shift = pages - g.kv_cache.shape[0]
+    big[shift:] = g.kv_cache
+    tables = torch.where(g.block_tables >= 0, g.block_tables + shift, g.block_tables)
+    dec = mla.MlaDecoder(3, 4, 32, 1500, "bf16", cuda_device, kernel=kernel, window=600, sinks=70)
+    results = []
+    for cache, table in ((g.kv_cache, g.block_tables), (big, tables)):
+        out, lse = dec(g.q, cache, table, g.seq_lens, g.softmax_scale)
+        w = dec.key_weights(g.q, cache, table, g.seq_lens, g.softmax_scale, lse,
+                            torch.zeros(3, 1500, device=cuda_device))
+        assert dec.status() == 0
+        results.append((out, lse, w))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    out_tables = torch.arange(12, dtype=torch.int32, device=cuda_device).view(3, 4) + shift - 12
+    _, kept, _ = mla.cache_evict(w, g.seq_lens, big, tables, big, out_tables, 256, 4, 100)
+    rows = big.view(-1, 576)
+    for b, want in enumerate(ref.evict(w, lens, 256, 4, 100)):
+        assert kept[b, :len(want)].tolist() == want
+        j, i = torch.tensor(want, device=cuda_device), torch.arange(len(want), device=cuda_device)
+        to = out_tables[b].long()[i // 64] * 64 + i % 64
+        assert torch.equal(rows[to], rows[tables[b].long()[j // 64] * 64 + j % 64])
